@@ -73,6 +73,7 @@ typedef enum {
 } ms_status;
 
 typedef enum { MS_F32 = 0, MS_BF16 = 1 } ms_dtype;
+typedef enum { MS_SOFTMAX = 0, MS_SIGMOID = 1 } ms_score;
 
 /* ---------------------------------------------------------------------- */
 /* a0  RMSNorm of the residual stream (the layer's normalised input).
@@ -111,6 +112,29 @@ MS_API ms_status moe_route_topk_tensor(const void* xhat, const float* w_router, 
                                        int T, int H, int E, int k, int renormalize,
                                        int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
                                        void* stream);
+
+/* a1 from given logits, with the choices of routers that balance their load
+ * by a bias and keep a token's experts within few groups.
+ *   s_e = softmax(z)_e or sigmoid(z_e);   c_e = s_e + select_bias[e]
+ *   the experts form n_groups groups of E/n_groups neighbours; a group's score
+ *   is the sum of its group_top (1 or 2) largest c, and the topk_groups best
+ *   groups stay (equal scores to the lower group);
+ *   topk_idx: the k largest c of those groups, descending, equal values to the
+ *   lower expert;  topk_w: s of the chosen experts (the bias only selects),
+ *   divided by their sum when renormalize != 0, times scale.
+ * Scores and selection are computed in fp64, so the choice does not depend on
+ * fp32 rounding.  A logit of -inf or NaN masks its expert: s = 0, ranked
+ * behind every other expert of the chosen groups (a masked expert counts 0 in
+ * its group's score, a group without any other expert ranks last), so that
+ * topk_idx always holds k different experts of the chosen groups, as
+ * moe_permute needs.  The bias is finite.
+ * logits: [T,E] fp32 or bf16 (any element alignment).  select_bias: [E] fp32
+ * or NULL.  topk_idx:
+ * [T,k] int32.  topk_w: [T,k] fp32.  E <= 256, E % n_groups == 0, n_groups <=
+ * 32, k <= 32, k <= topk_groups * E / n_groups.  No scratch. */
+MS_API ms_status moe_route_grouped(const void* logits, ms_dtype logits_dtype, const float* select_bias, int T, int E,
+                                   ms_score score, int n_groups, int topk_groups, int group_top, int k,
+                                   int renormalize, float scale, int32_t* topk_idx, float* topk_w, void* stream);
 
 /* a2  Permutation: group the T*k (token, slot) pairs by expert, ordered by
  * (expert, token) -- a stable counting sort, bit-exact and deterministic.
@@ -212,6 +236,62 @@ MS_API size_t spec_verify_workspace_size(int B, int K, int V);
 MS_API ms_status spec_verify_greedy(const void* logits, ms_dtype logits_dtype, const int32_t* draft,
                              int B, int K, int V, int32_t* argmax, int32_t* committed,
                              int32_t* n_committed, void* ws, size_t ws_bytes, void* stream);
+
+/* Sampling: one token per logits row, from given uniform random numbers.
+ * Row r's weights are w_v = exp((l_v - max l) / temperature[r]); NaN logits
+ * count as -inf, weights under 2^-64 of the largest as zero.  Of these,
+ *   min_p   keeps the tokens whose weight is at least min_p of the largest,
+ *   top_k   keeps the first top_k tokens in the order (larger logit, lower index),
+ *   top_p   keeps the shortest prefix of that order whose weights reach top_p
+ *           times the sum over the tokens kept so far (at least one token),
+ * in this order.  token[r] is the first index, in ascending index order, whose
+ * cumulative kept weight exceeds u[r] times the sum of the kept weights.
+ * probs[r,v] = w_v / that sum, 0 where not kept (what spec_verify_sample takes
+ * as draft_probs).
+ * Weights and sums are computed beyond fp32 (about 1e-13, fixed order), so a
+ * token does not depend on rounding, the batch or the run.
+ * A temperature that is not above 0 (0, negative, NaN) makes its row greedy:
+ * the lowest index among the largest logits.  top_k <= 0 or >= V, top_p >= 1
+ * or NaN, min_p <= 0 or NaN leave their filter out; min_p > 1 counts as 1,
+ * top_p <= 0 keeps one token.  Tokens at +inf share the whole weight.  A row
+ * without any logit above -inf gives token -1 and probabilities 0.
+ * temperature is finite; u lies in [0, 1).
+ * logits: [T,V] fp32 or bf16 (any element alignment).  temperature, top_p, min_p, u: [T] fp32, top_k:
+ * [T] int32; each but u may be NULL (temperature 1, filter left out).
+ * token: [T] int32.  probs: [T,V] fp32 or NULL.  V <= 262,144, T <= 2^24.
+ * No scratch. */
+MS_API ms_status spec_sample(const void* logits, ms_dtype logits_dtype, int T, int V, const float* temperature,
+                             const int32_t* top_k, const float* top_p, const float* min_p, const float* u,
+                             int32_t* token, float* probs, void* stream);
+
+/* Speculative verification of sampled decoding: the committed tokens follow
+ * the distribution that spec_sample draws from, whatever drafted them (greedy
+ * verification, spec_verify_greedy, is lossless for greedy decoding only).
+ * With p_j the distribution of spec_sample for row (b, j) under sequence b's
+ * parameters and q_j = draft_probs[b,j,:] the one that draft[b,j] was drawn
+ * from (draft_probs NULL: the draft was certain, q_j = 1 at the draft, as
+ * fastmtp_draft's):
+ *   draft j is accepted iff u[b,j] * q_j(draft) < p_j(draft);
+ *   at the first rejected position the committed token is drawn from
+ *   max(p_j - q_j, 0), with all K accepted from p_K, both as spec_sample draws
+ *   (cumulative weight in index order against u[b,K] times the sum); where
+ *   max(p_j - q_j, 0) is zero everywhere, from p_j.
+ * committed[b,:] = the accepted drafts, the drawn token, then -1 padding;
+ * n_committed[b] = how many of them are tokens: 1..K+1 (one less where the
+ * drawn row has no logit above -inf: its token is -1).  A draft outside [0, V)
+ * is rejected.
+ * logits: [B,K+1,V] fp32 or bf16 (any element alignment).  draft: [B,K] int32.  draft_probs: [B,K,V]
+ * fp32 or NULL.  temperature, top_p, min_p: [B] fp32, top_k: [B] int32, each
+ * NULL or as in spec_sample.  u: [B,K+1] fp32 in [0, 1), independent.
+ * committed: [B,K+1] int32.  n_committed: [B] int32.  K = 0 (draft may be
+ * NULL) is plain sampling.  K <= 8, V <= 262,144, B*(K+1) <= 2^24.
+ * Scratch: spec_verify_sample_workspace_size(B,K,V) bytes. */
+MS_API size_t spec_verify_sample_workspace_size(int B, int K, int V);
+MS_API ms_status spec_verify_sample(const void* logits, ms_dtype logits_dtype, const int32_t* draft,
+                                    const float* draft_probs, const float* temperature, const int32_t* top_k,
+                                    const float* top_p, const float* min_p, const float* u, int B, int K, int V,
+                                    int32_t* committed, int32_t* n_committed, void* ws, size_t ws_bytes,
+                                    void* stream);
 
 /* a5 + a6 fused: the vocab head with the verification's argmax in its
  * epilogue, then the prefix match -- the logits are never written.

@@ -35,7 +35,8 @@ static const char* kNames[K_COUNT] = {
     "rmsnorm",        "route_rows",      "route_tiled",     "route_cluster", "permute_count", "permute_scatter",
     "ffn_prep",       "gemm1_stream",    "gemm2_stream",    "gemm1_tiled",   "gemm2_tiled",  "ffn_finish",
     "lm_head_stream", "combine",         "verify_partial",  "verify_final",  "verify_cluster", "verify_keys", "wait_probe",
-    "pack_weights",   "mtp_prep",        "moe_stream_layer", "route_tc",     "route_split"};
+    "pack_weights",   "mtp_prep",        "moe_stream_layer", "route_tc",     "route_split",
+    "route_grouped",  "sample",          "sample_verify",   "sample_commit"};
 
 const char* kernel_name(int id) { return (id >= 0 && id < K_COUNT) ? kNames[id] : "?"; }
 

@@ -39,6 +39,10 @@ enum KernelId : int {
     K_LAYER_FUSED,
     K_ROUTE_TC,
     K_ROUTE_SPLIT,
+    K_ROUTE_GROUPED,
+    K_SAMPLE,
+    K_SAMPLE_VERIFY,
+    K_SAMPLE_COMMIT,
     K_COUNT
 };
 const char* kernel_name(int id);
@@ -160,6 +164,10 @@ inline int num_sms() {
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline bool element_aligned(const void* p, ms_dtype dt) {
+    return (reinterpret_cast<uintptr_t>(p) & (dt == MS_BF16 ? 1u : 3u)) == 0;
+}
 
 // ------------------------------------------------------------ device side
 // Wait for the kernel this one depends on (no-op when launched without PDL).

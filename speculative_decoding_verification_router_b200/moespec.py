@@ -17,6 +17,7 @@ import torch
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoespec.so")
 
 MS_F32, MS_BF16 = 0, 1
+MS_SOFTMAX, MS_SIGMOID = 0, 1
 STATUS = {0: "MS_OK", -1: "MS_ERR_INVALID_ARG", -2: "MS_ERR_UNSUPPORTED", -3: "MS_ERR_WORKSPACE",
           -4: "MS_ERR_CUDA", -5: "MS_ERR_TIMEOUT", -6: "MS_ERR_DEVICE_INDEX",
           -7: "MS_ERR_DRAIN_TIMEOUT"}
@@ -47,6 +48,10 @@ def _load():
         "moe_expert_ffn_workspace_size": (Z, [I, I, I, I, I, I]),
         "moe_expert_ffn": (I, [P, P, P, P, P, P, P, I, I, I, I, I, I, P, I, P, P, Z, P]),
         "moe_combine": (I, [P, I, P, P, P, P, I, I, I, P, P, P]),
+        "moe_route_grouped": (I, [P, I, P, I, I, I, I, I, I, I, I, F, P, P, P]),
+        "spec_sample": (I, [P, I, I, I, P, P, P, P, P, P, P, P]),
+        "spec_verify_sample_workspace_size": (Z, [I, I, I]),
+        "spec_verify_sample": (I, [P, I, P, P, P, P, P, P, P, I, I, I, P, P, P, Z, P]),
         "lm_head_workspace_size": (Z, [I, I, I]),
         "lm_head_logits": (I, [P, P, I, I, I, P, P, Z, P]),
         "spec_verify_workspace_size": (Z, [I, I, I]),
@@ -112,6 +117,64 @@ def _dev(t: torch.Tensor, dtype, name: str):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
+
+
+_LOGITS = {torch.float32: MS_F32, torch.bfloat16: MS_BF16}
+_SCORES = {"softmax": MS_SOFTMAX, "sigmoid": MS_SIGMOID}
+
+
+def _a(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dims: int):
+    """Checks a logits tensor; returns its shape."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _LOGITS:
+        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.shape
+
+
+def _vec(t: torch.Tensor, dtype, shape, name: str, dev):
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _filters(n: int, dev, temperature, top_k, top_p, min_p):
+    if temperature is not None:
+        _vec(temperature, torch.float32, (n,), "temperature", dev)
+    if top_k is not None:
+        _vec(top_k, torch.int32, (n,), "top_k", dev)
+    if top_p is not None:
+        _vec(top_p, torch.float32, (n,), "top_p", dev)
+    if min_p is not None:
+        _vec(min_p, torch.float32, (n,), "min_p", dev)
+
+
+class _Here:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_here = _Here()
+
+
+def _on(dev):
+    """Makes a tensor's device current for the call (a no-op where it already is)."""
+    return _here if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _raw_stream(dev, stream):
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
 
 
 class Workspace:
@@ -217,6 +280,33 @@ def route_topk_tensor(xhat: torch.Tensor, w_router: torch.Tensor, bias=None, k: 
     return idx, w
 
 
+def route_grouped(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+                  n_groups: int = 1, topk_groups: Optional[int] = None, group_top: int = 1,
+                  renormalize: bool = False, scale: float = 1.0, out=None, stream=None):
+    """Expert choice from router logits [T, E] (fp32 or bf16) by "softmax" or "sigmoid"
+    scores, a selection bias [E], expert groups, top-k and scaled weights.
+    Returns (topk_idx [T, k] int32, topk_w [T, k] fp32)."""
+    T, E = _rows(logits, "logits", 2)
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    dev = logits.device
+    if bias is not None:
+        _vec(bias, torch.float32, (E,), "bias", dev)
+    if out is None:
+        idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    else:
+        idx, w = out
+        _vec(idx, torch.int32, (T, k), "out[0]", dev)
+        _vec(w, torch.float32, (T, k), "out[1]", dev)
+    with _on(dev):
+        _check(_lib.moe_route_grouped(logits.data_ptr(), _LOGITS[logits.dtype], _a(bias), T, E, _SCORES[score],
+                                      n_groups, n_groups if topk_groups is None else topk_groups, group_top, k,
+                                      int(renormalize), scale, idx.data_ptr(), w.data_ptr(), _raw_stream(dev, stream)),
+               "moe_route_grouped")
+    return idx, w
+
+
 def permute(idx: torch.Tensor, E: int, ws: Optional[Workspace] = None, out=None, stream=None):
     _dev(idx, torch.int32, "topk_idx")
     T, k = idx.shape
@@ -297,6 +387,61 @@ def verify_greedy(logits, draft, ws: Optional[Workspace] = None, out=None, strea
     _check(_lib.spec_verify_greedy(_p(logits), dt, _p(draft), B, K, V, _p(am), _p(cm), _p(n), w.c(), w.nbytes,
                                    _stream(stream)), "spec_verify_greedy")
     return am, cm, n
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None,
+           return_probs: bool = False, out=None, stream=None):
+    """One token per row of logits [T, V] (fp32 or bf16) from uniform numbers u [T] in
+    [0, 1), under per-row temperature, top_k, top_p and min_p ([T] tensors or None).
+    Returns token [T] int32, or (token, probs [T, V] fp32) with return_probs."""
+    T, V = _rows(logits, "logits", 2)
+    dev = logits.device
+    _vec(u, torch.float32, (T,), "u", dev)
+    _filters(T, dev, temperature, top_k, top_p, min_p)
+    if out is None:
+        token = torch.empty(T, dtype=torch.int32, device=dev)
+        probs = torch.empty((T, V), dtype=torch.float32, device=dev) if return_probs else None
+    else:
+        token, probs = out if return_probs else (out, None)
+        _vec(token, torch.int32, (T,), "out token", dev)
+        if probs is not None:
+            _vec(probs, torch.float32, (T, V), "out probs", dev)
+    with _on(dev):
+        _check(_lib.spec_sample(logits.data_ptr(), _LOGITS[logits.dtype], T, V, _a(temperature), _a(top_k), _a(top_p),
+                                _a(min_p), u.data_ptr(), token.data_ptr(), _a(probs), _raw_stream(dev, stream)),
+               "spec_sample")
+    return (token, probs) if return_probs else token
+
+
+def verify_sample(logits: torch.Tensor, draft: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None,
+                  top_p=None, min_p=None, draft_probs: Optional[torch.Tensor] = None,
+                  ws: Optional[Workspace] = None, out=None, stream=None):
+    """Speculative verification of sampled decoding: logits [B, K+1, V] (fp32 or bf16),
+    draft [B, K] int32, u [B, K+1] in [0, 1), per-sequence temperature, top_k, top_p,
+    min_p ([B] tensors or None), draft_probs [B, K, V] fp32 (None: the drafts were
+    certain).  Returns (committed [B, K+1] int32, n_committed [B] int32)."""
+    B, K1, V = _rows(logits, "logits", 3)
+    K = K1 - 1
+    dev = logits.device
+    _vec(draft, torch.int32, (B, K), "draft", dev)
+    _vec(u, torch.float32, (B, K1), "u", dev)
+    _filters(B, dev, temperature, top_k, top_p, min_p)
+    if draft_probs is not None:
+        _vec(draft_probs, torch.float32, (B, K, V), "draft_probs", dev)
+    if out is None:
+        cm = torch.empty((B, K1), dtype=torch.int32, device=dev)
+        n = torch.empty(B, dtype=torch.int32, device=dev)
+    else:
+        cm, n = out
+        _vec(cm, torch.int32, (B, K1), "out[0]", dev)
+        _vec(n, torch.int32, (B,), "out[1]", dev)
+    w = _ws(ws, _lib.spec_verify_sample_workspace_size(B, K, V), dev)
+    with _on(dev):
+        _check(_lib.spec_verify_sample(logits.data_ptr(), _LOGITS[logits.dtype], draft.data_ptr() if K else None,
+                                       _a(draft_probs), _a(temperature), _a(top_k), _a(top_p), _a(min_p),
+                                       u.data_ptr(), B, K, V, cm.data_ptr(), n.data_ptr(), w.ptr, w.nbytes,
+                                       _raw_stream(dev, stream)), "spec_verify_sample")
+    return cm, n
 
 
 def verify_lm_head_greedy(xhat, w_lm, draft, ws: Optional[Workspace] = None, out=None, stream=None):

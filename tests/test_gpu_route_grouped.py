@@ -1,0 +1,118 @@
+"""GPU parity of moe_route_grouped against the 64-bit oracle: the chosen experts
+exactly; the gate weights to fp32 evaluation, 16 x 2^-24 relative (an exp within
+2 ulp, a tree sum of at most 256 positive terms, two divisions, the scale)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import sampling as sp
+from speculative_decoding_verification_router_b200 import synth
+from tests.gpu_util import assert_close, dev, host
+from tests.inputs import routed_layer_inputs
+
+pytestmark = pytest.mark.gpu
+
+REL = 16 * 2.0 ** -24
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def ms():
+    from speculative_decoding_verification_router_b200 import moespec
+    return moespec
+
+
+def _logits(g, T, E):
+    z = 2 * g.standard_normal((T, E))
+    special = [np.zeros(E), np.full(E, -np.inf), np.full(E, np.nan), np.full(E, -1e38), 50 + g.standard_normal(E),
+               -50 - g.standard_normal(E), np.round(g.standard_normal(E)),
+               np.where(g.random(E) < 0.9, -np.inf, g.standard_normal(E)),
+               np.where(g.random(E) < 0.5, np.nan, g.standard_normal(E)),
+               np.where(g.random(E) < 0.2, np.inf, g.standard_normal(E))]
+    z[: len(special)] = special[: T]
+    return z.astype(np.float32)
+
+
+def _check(ms, z, k, dtype, **kw):
+    t = torch.from_numpy(z).to(DTYPES[dtype])
+    bias = kw.pop("bias")
+    idx, w = ms.route_grouped(t.cuda(), k, bias=None if bias is None else dev(bias), **kw)
+    torch.cuda.synchronize()
+    ri, rw = sp.route(t.float().numpy(), k, bias=bias, **kw)
+    np.testing.assert_array_equal(host(idx), ri)
+    assert np.all(np.abs(host(w).astype(np.float64) - rw) <= REL * rw + 1e-37)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(1, 1), (2, 1), (8, 2), (40, 4), (64, 8), (96, 1), (160, 4), (256, 8), (256, 32)])
+def test_route_grouped_matches_the_oracle(ms, E, groups, score, dtype):
+    g = np.random.default_rng(E + groups)
+    z = _logits(g, 67, E)
+    for tg in sorted({1, (groups + 1) // 2, groups}):
+        for top, renorm in ((1, False), (2, True)):
+            k = int(g.integers(1, min(32, tg * (E // groups)) + 1))
+            bias = (0.1 * g.standard_normal(E)).astype(np.float32) if top == 2 else None
+            _check(ms, z, k, dtype, bias=bias, score=score, n_groups=groups, topk_groups=tg, group_top=top,
+                   renormalize=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("T", [1, 7, 9, 36992])
+def test_route_grouped_token_counts(ms, T):
+    g = np.random.default_rng(T)
+    z = 2 * g.standard_normal((T, 64)).astype(np.float32)
+    bias = (0.1 * g.standard_normal(64)).astype(np.float32)
+    kw = dict(score="sigmoid", n_groups=8, topk_groups=3, group_top=2, renormalize=True)
+    idx, w = ms.route_grouped(dev(z), 6, bias=dev(bias), **kw)
+    at = np.unique(np.r_[0, T - 1, g.integers(0, T, 200)])
+    ri, rw = sp.route(z[at], 6, bias=bias, **kw)
+    np.testing.assert_array_equal(host(idx)[at], ri)
+    assert np.all(np.abs(host(w)[at] - rw) <= REL * rw)
+
+
+def test_close_scores_are_told_apart(ms):
+    # neighbours in fp32 around 0 give sigmoid scores a quarter of a step apart: equal in fp32, not in truth
+    E = 64
+    z = np.full((1, E), -1.0, np.float32)
+    z[0, 10:20] = np.float32(0.4) + np.arange(10, dtype=np.float32) * np.float32(2.0 ** -25)
+    _check(ms, z, 6, "f32", bias=None, score="sigmoid")
+    bias = np.zeros(E, np.float32)
+    bias[10:20] = 0.25
+    _check(ms, z, 6, "f32", bias=bias, score="sigmoid")
+
+
+def test_softmax_without_groups_is_route_topk(ms):
+    g = np.random.default_rng(1)
+    H, E, T = 256, 64, 50
+    x = ms.rmsnorm(dev(g.standard_normal((T, H)).astype(np.float32)))
+    eye = torch.zeros(E, H, device="cuda")
+    eye[:, :E] = torch.eye(E, device="cuda")        # the logits are the first E activations, exactly
+    idx, w = ms.route_topk(x, eye, k=6, renormalize=True)
+    gi, gw = ms.route_grouped(x[:, :E].contiguous(), 6, renormalize=True)
+    assert torch.equal(idx, gi)
+    torch.testing.assert_close(w, gw, rtol=2 * REL, atol=0)
+
+
+def test_routed_layer_with_grouped_experts(ms):
+    """rmsnorm -> router logits -> moe_route_grouped -> permute -> experts -> combine, against the oracle's experts
+    under the oracle's routing."""
+    shp = synth.MoEShape("grouped", B=8, K=3, H=256, E=16, I=128, k=4, S=1, V=256, router_std=0.2)
+    a, lw, _ = routed_layer_inputs(shp, 0)
+    x = ms.rmsnorm(dev(a))
+    z = x.float() @ dev(lw.w_router).t()
+    bias = (0.05 * np.random.default_rng(4).standard_normal(shp.E)).astype(np.float32)
+    kw = dict(score="sigmoid", n_groups=4, topk_groups=2, group_top=2, renormalize=True, scale=2.0)
+    idx, w = ms.route_grouped(z, shp.k, bias=dev(bias), **kw)
+    off, perm, slot = ms.permute(idx, shp.E)
+    pk = lambda t: ms.pack_weights(dev(t))   # noqa: E731
+    y, ysh = ms.expert_ffn(x, off, perm, pk(lw.w_gate_up), pk(lw.w_down), pk(lw.ws_gate_up), pk(lw.ws_down), shp.k)
+    out = ms.combine(y, ysh, slot, w, dev(a))
+    torch.cuda.synchronize()
+    xh = host(x)
+    ri, rw = sp.route(host(z), shp.k, bias=bias, **kw)
+    ro, rp, rs = oracle.permute(ri, shp.E)
+    ry = oracle.expert_ffn_routed(xh, lw.w_gate_up, lw.w_down, ro, rp, shp.k)
+    rsh = oracle.expert_ffn_shared(xh, lw.ws_gate_up, lw.ws_down)
+    np.testing.assert_array_equal(host(idx), ri)
+    assert_close(host(out), oracle.combine(ry, rsh, rs, rw.astype(np.float32), a), what="layer")

@@ -1,0 +1,344 @@
+"""GPU parity of spec_sample and spec_verify_sample against the 64-bit oracle.
+
+Tokens are compared exactly: the kernels decide in more than fp32, so that a
+draw differs from the oracle's only where u times the total lies within about
+1e-12 of a border of the cumulative sum.  probs is the fp64 quotient rounded to
+fp32 once: half a step, 2^-24 relative, and 1e-11 for the weights themselves."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import sampling as sp
+from speculative_decoding_verification_router_b200 import synth
+from tests.gpu_util import dev, host
+
+pytestmark = pytest.mark.gpu
+
+REL = 2.0 ** -24 + 1e-11
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def ms():
+    from speculative_decoding_verification_router_b200 import moespec
+    return moespec
+
+
+def _row(g, kind, V):
+    """One logits row of a kind that a filter can go wrong on."""
+    if kind == "peaked":
+        return 1.5 * g.exponential(size=V) + 0.5 * g.standard_normal(V)
+    if kind == "zeros":
+        return np.zeros(V)
+    if kind == "tiny":                      # all weights nearly equal, keys spread over many exponents
+        return g.standard_normal(V) * 1e-5
+    if kind == "two":                       # two values only: ties at every border
+        return g.integers(0, 2, V).astype(float)
+    if kind == "lowest":
+        return np.full(V, float(np.finfo(np.float32).min))
+    if kind == "huge":
+        return g.standard_normal(V) * 1e30
+    if kind == "one":                       # a single token far above the rest
+        x = g.standard_normal(V) - 20
+        x[g.integers(V)] = 10
+        return x
+    x = g.standard_normal(V) * 3
+    if kind == "masked":
+        x[g.random(V) < 0.9] = -np.inf
+    elif kind == "nan":
+        x[g.random(V) < 0.3] = np.nan
+    elif kind == "inf":
+        x[g.random(V) < 0.1] = np.inf
+    elif kind == "empty":
+        x[:] = -np.inf
+        x[:: 2] = np.nan
+    return x
+
+
+KINDS = ["normal", "peaked", "zeros", "tiny", "two", "lowest", "huge", "one", "masked", "nan", "inf", "empty"]
+
+
+def _params(g, n, V):
+    at = lambda v: np.array([v[g.integers(len(v))] for _ in range(n)])   # noqa: E731
+    return dict(temperature=at([1.0, 0.7, 0.0, -1.0, 2.0, 1e-3, 100.0, 1.0]).astype(np.float32),
+                top_k=at([0, 0, 1, 5, 40, V, V - 1, V + 5, max(1, V // 2), 600, 2500]).astype(np.int32),
+                top_p=at([1.0, 1.0, 0.5, 0.9, 0.99, 0.0, -1.0, 1e-6, 2.0]).astype(np.float32),
+                min_p=at([0.0, 0.0, 0.1, 1.0, 2.0, 1e-9]).astype(np.float32))
+
+
+def _logits(g, V, per_kind, dtype):
+    z = np.stack([_row(g, k, V) for k in KINDS for _ in range(per_kind)])
+    with np.errstate(over="ignore"):
+        t = torch.from_numpy(z.astype(np.float32)).to(DTYPES[dtype])
+    return t.cuda(), t.float().numpy()
+
+
+def _uniform(g, shape):
+    u = (g.integers(0, 1 << 24, shape) * 2.0 ** -24).astype(np.float32)
+    u[g.random(shape) < 0.1] = 0.0
+    u[g.random(shape) < 0.1] = 1.0 - 2.0 ** -24
+    return u
+
+
+def _on(p):
+    return {n: None if v is None else dev(v) for n, v in p.items()}
+
+
+def _assert_probs(got, want):
+    assert np.all(np.abs(got.astype(np.float64) - want) <= REL * want), np.abs(got - want).max()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 33, 1000, 1025, 4099, 20001])
+def test_sample_matches_the_oracle(ms, V, dtype):
+    g = np.random.default_rng(V)
+    z, zh = _logits(g, V, 4, dtype)
+    par = _params(g, len(zh), V)
+    u = _uniform(g, len(zh))
+    tok, probs = ms.sample(z, dev(u), **_on(par), return_probs=True)
+    only = ms.sample(z, dev(u), **_on(par))
+    torch.cuda.synchronize()
+    want, wp = sp.sample(zh, u, **par)
+    np.testing.assert_array_equal(host(tok), want)
+    np.testing.assert_array_equal(host(only), want)
+    _assert_probs(host(probs), wp)
+
+
+FILTERS = {
+    "temperature": dict(temperature=0.8), "nothing": dict(), "greedy": dict(temperature=0.0),
+    "top_k": dict(top_k=50), "wide_top_k": dict(temperature=1.1, top_k=5000), "top_p": dict(top_p=0.9),
+    "wide_top_p": dict(temperature=1.5, top_p=0.98), "min_p": dict(min_p=0.05),
+    "all": dict(temperature=0.7, top_k=40, top_p=0.95, min_p=0.02),
+    "wide_both": dict(temperature=1.5, top_k=20000, top_p=0.9)}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", list(FILTERS))
+def test_sample_full_vocabulary(ms, name, dtype):
+    V, R = 129280, 6
+    g = np.random.default_rng(7)
+    z = torch.from_numpy((g.exponential(size=(R, V)) * np.linspace(0.7, 1.8, R)[:, None] - 2).astype(np.float32))
+    z = z.to(DTYPES[dtype])
+    u = _uniform(g, R)
+    par = {n: np.full(R, v, np.int32 if n == "top_k" else np.float32) for n, v in FILTERS[name].items()}
+    tok, probs = ms.sample(z.cuda(), dev(u), **_on(par), return_probs=True)
+    torch.cuda.synchronize()
+    want, wp = sp.sample(z.float().numpy(), u, **par)
+    np.testing.assert_array_equal(host(tok), want)
+    _assert_probs(host(probs), wp)
+
+
+@pytest.mark.parametrize("V", [262144, 200001])
+def test_sample_largest_vocabulary(ms, V):
+    g = np.random.default_rng(9)
+    z = torch.from_numpy(g.standard_normal((2, V)).astype(np.float32))
+    u = _uniform(g, 2)
+    par = dict(temperature=np.array([1.0, 3.0], np.float32), top_p=np.array([1.0, 0.97], np.float32))
+    tok = ms.sample(z.cuda(), dev(u), **_on(par))
+    np.testing.assert_array_equal(host(tok), sp.sample(z.numpy(), u, **par)[0])
+
+
+def test_equal_weights_are_split_exactly(ms):
+    # the border cases that rounding would decide: 2n equal weights, top_p 0.5 keeps n, u = i / 2n draws token i
+    for n in (4, 512, 4096):
+        V = 2 * n
+        z = torch.full((V, V), 0.3, device="cuda")
+        u = torch.arange(V, device="cuda", dtype=torch.float32) / V
+        tok = ms.sample(z, u)
+        assert torch.equal(tok, torch.arange(V, device="cuda", dtype=torch.int32))
+        half = torch.full((V,), 0.5, device="cuda")
+        _, p = ms.sample(z, u, top_p=half, return_probs=True)
+        assert torch.equal((p > 0).sum(1), torch.full((V,), n, device="cuda"))
+        assert bool((p[:, :n] > 0).all())
+
+
+def test_sample_does_not_depend_on_the_batch_or_the_run(ms):
+    g = np.random.default_rng(2)
+    z, _ = _logits(g, 5003, 8, "bf16")
+    n = z.shape[0]
+    par, u = _on(_params(g, n, 5003)), dev(_uniform(g, n))
+    a = ms.sample(z, u, **par, return_probs=True)
+    b = ms.sample(z, u, **par, return_probs=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for r in range(0, n, 5):
+        t, p = ms.sample(z[r:r + 1], u[r:r + 1], **{k: v[r:r + 1] for k, v in par.items()}, return_probs=True)
+        assert torch.equal(t, a[0][r:r + 1]) and torch.equal(p, a[1][r:r + 1])
+
+
+def test_sample_writes_only_its_rows(ms):
+    V = 777
+    z = torch.randn(3, V, device="cuda")
+    probs = torch.full((5, V), 7.0, device="cuda")
+    tok = torch.full((5,), 7, dtype=torch.int32, device="cuda")
+    ms.sample(z, torch.rand(3, device="cuda"), return_probs=True, out=(tok[1:4], probs[1:4]))
+    assert bool((probs[[0, 4]] == 7).all()) and bool((tok[[0, 4]] == 7).all())
+
+
+def test_sample_on_another_stream_and_captured(ms):
+    V, R = 20000, 5
+    z = torch.randn(R, V, device="cuda") * 3
+    u, tok = torch.rand(R, device="cuda"), torch.empty(R, dtype=torch.int32, device="cuda")
+    top_p = torch.full((R,), 0.9, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ms.sample(z, u, top_p=top_p, out=tok, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(tok, ms.sample(z, u, top_p=top_p))
+    graph = ms.CapturedStep(lambda: ms.sample(z, u, top_p=top_p, out=tok))
+    for seed in range(3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        z.normal_(generator=g).mul_(3)
+        u.uniform_(generator=g)
+        torch.cuda.synchronize()
+        graph()
+        torch.cuda.synchronize()
+        assert torch.equal(tok, ms.sample(z, u, top_p=top_p))
+
+
+# ---------------------------------------------------------------- verification
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("with_q", [False, True])
+@pytest.mark.parametrize("V,K", [(1, 1), (5, 2), (129, 1), (1003, 3), (4099, 8), (20001, 3)])
+def test_verify_sample_matches_the_oracle(ms, V, K, with_q, dtype):
+    g = np.random.default_rng(V + K)
+    z, zh = _logits(g, V, K + 1, dtype)
+    g.shuffle(perm := np.arange(len(zh)))
+    B = len(zh) // (K + 1)
+    z = z[torch.from_numpy(perm[: B * (K + 1)]).cuda()].view(B, K + 1, V).contiguous()
+    zh = zh[perm[: B * (K + 1)]].reshape(B, K + 1, V)
+    par, u = _params(g, B, V), _uniform(g, (B, K + 1))
+    best = np.nan_to_num(zh[:, :K], nan=-np.inf).argmax(-1)
+    d = np.where(g.random((B, K)) < 0.6, best, g.integers(-2, V + 2, (B, K))).astype(np.int32)
+    q = None
+    if with_q:
+        q = g.random((B, K, V)) ** 8
+        q = (q / q.sum(-1, keepdims=True)).astype(np.float32)
+    cm, n = ms.verify_sample(z, dev(d), dev(u), draft_probs=None if q is None else dev(q), **_on(par))
+    torch.cuda.synchronize()
+    wcm, wn = sp.verify(zh, d, u, q, **par)
+    np.testing.assert_array_equal(host(cm), wcm)
+    np.testing.assert_array_equal(host(n), wn)
+
+
+@pytest.mark.parametrize("par", [dict(temperature=0.8), dict(temperature=1.2, top_p=0.95), dict(top_k=50, top_p=0.9)],
+                         ids=["temperature", "top_p", "top_k_p"])
+@pytest.mark.parametrize("with_q", [False, True])
+def test_verify_sample_full_vocabulary(ms, par, with_q):
+    B, K, V = 3, 3, 129280
+    g = np.random.default_rng(11)
+    z = torch.from_numpy((g.exponential(size=(B, K + 1, V)) * 1.2).astype(np.float32)).bfloat16()
+    zh = z.float().numpy()
+    par = {n: np.full(B, v, np.int32 if n == "top_k" else np.float32) for n, v in par.items()}
+    u = _uniform(g, (B, K + 1))
+    d = zh[:, :K].argmax(-1).astype(np.int32)
+    q = None
+    if with_q:
+        q = np.exp(zh[:, :K] + g.standard_normal((B, K, V)))
+        q = (q / q.sum(-1, keepdims=True)).astype(np.float32)
+    cm, n = ms.verify_sample(z.cuda(), dev(d), dev(u), draft_probs=None if q is None else dev(q), **_on(par))
+    wcm, wn = sp.verify(zh, d, u, q, **par)
+    np.testing.assert_array_equal(host(cm), wcm)
+    np.testing.assert_array_equal(host(n), wn)
+
+
+def test_greedy_rows_verify_as_spec_verify_greedy(ms):
+    B, K, V = 16, 3, 4096
+    z = torch.randn(B, K + 1, V, device="cuda").bfloat16()
+    d = z[:, :K].float().argmax(-1).int()
+    d[::3, 1] += 1
+    d.clamp_(max=V - 1)
+    zero = torch.zeros(B, device="cuda")
+    cm, n = ms.verify_sample(z, d, torch.rand(B, K + 1, device="cuda"), temperature=zero)
+    _, gcm, gn = ms.verify_greedy(z, d)
+    assert torch.equal(cm, gcm) and torch.equal(n, gn)
+
+
+def test_no_drafts_is_plain_sampling(ms):
+    B, V = 40, 3001
+    z, u = torch.randn(B, 1, V, device="cuda"), torch.rand(B, 1, device="cuda")
+    t = torch.full((B,), 0.9, device="cuda")
+    cm, n = ms.verify_sample(z, torch.empty((B, 0), dtype=torch.int32, device="cuda"), u, temperature=t)
+    assert torch.equal(cm[:, 0], ms.sample(z[:, 0], u[:, 0], temperature=t)) and bool((n == 1).all())
+
+
+@pytest.mark.parametrize("certain", [False, True])
+def test_committed_tokens_follow_the_sampled_distribution(ms, certain):
+    """Draft with spec_sample, verify with spec_verify_sample, B times on the same rows: the first committed
+    token's counts are binomial with p_0, so each lies within 6 standard deviations (two in 10^9 a token)."""
+    V, B, K = 24, 60000, 2
+    g = torch.Generator(device="cuda").manual_seed(5)
+    z1 = 1.5 * torch.randn(1, K + 1, V, generator=g, device="cuda")
+    zd = z1[:, :K] + torch.randn(1, K, V, generator=g, device="cuda")
+    z = z1.expand(B, K + 1, V).contiguous()
+    top_p, t = torch.full((B,), 0.9, device="cuda"), torch.full((B,), 0.8, device="cuda")
+    if certain:
+        d, q = zd.argmax(-1).int().expand(B, K).contiguous(), None
+    else:
+        d, q = ms.sample(zd.expand(B, K, V).reshape(B * K, V), torch.rand(B * K, generator=g, device="cuda"),
+                         return_probs=True)
+        d, q = d.view(B, K), q.view(B, K, V)
+    cm, n = ms.verify_sample(z, d, torch.rand(B, K + 1, generator=g, device="cuda"), temperature=t, top_p=top_p,
+                             draft_probs=q)
+    p = sp.distribution(host(z1)[0, 0], 0.800000011920929, 0, 0.8999999761581421)
+    p /= p.sum()
+    got = np.bincount(host(cm)[:, 0], minlength=V) / B
+    assert np.all(np.abs(got - p) <= 6 * np.sqrt(p * (1 - p) / B) + 1e-12), (got, p)
+    assert 1 < float(n.float().mean()) < K + 1
+
+
+def test_verify_sample_captured_with_its_own_workspace(ms):
+    B, K, V = 4, 3, 30011
+    z, u = torch.empty(B, K + 1, V, device="cuda"), torch.empty(B, K + 1, device="cuda")
+    d = torch.zeros(B, K, dtype=torch.int32, device="cuda")
+    k = torch.full((B,), 20, dtype=torch.int32, device="cuda")
+    ws = ms.Workspace(ms.lib().spec_verify_sample_workspace_size(B, K, V))
+    ws.view().fill_(0xff)
+    out = (torch.empty(B, K + 1, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda"))
+    z.normal_()
+    u.uniform_()
+    graph = ms.CapturedStep(lambda: ms.verify_sample(z, d, u, top_k=k, ws=ws, out=out))
+    for seed in range(3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        z.normal_(generator=g).mul_(2)
+        u.uniform_(generator=g)
+        d.copy_(z[:, :K].argmax(-1))
+        torch.cuda.synchronize()
+        graph()
+        torch.cuda.synchronize()
+        cm, n = ms.verify_sample(z, d, u, top_k=k)
+        assert torch.equal(out[0], cm) and torch.equal(out[1], n)
+
+
+def test_draft_head_sampled_verify_chain(ms):
+    """A speculative step of sampled decoding through the library: FastMTP drafts (certain), the vocabulary head
+    over the verify rows, sampled verification of its logits."""
+    B, H, I, V, K = 4, 256, 128, 1024, 3
+    n = lambda name, shape, std: dev(synth.normal_bf16(3, name, shape, std))   # noqa: E731
+    pk = ms.pack_weights
+    emb, w_lm = n("e", (V, H), 1.0), pk(n("lm", (V, H), 0.2))
+    drafts, h = ms.fastmtp_draft(torch.randn(B, H, device="cuda"), torch.arange(B, dtype=torch.int32, device="cuda"),
+                                 emb, pk(n("p", (H, 2 * H), 0.05)), pk(n("gu", (2 * I, H), 0.05)),
+                                 pk(n("d", (H, I), 0.05)), w_lm, K)
+    x = ms.rmsnorm(torch.randn(B * (K + 1), H, device="cuda"))
+    logits = ms.lm_head(x, w_lm).view(B, K + 1, V)
+    u = torch.rand(B, K + 1, device="cuda")
+    par = dict(temperature=np.full(B, 0.9, np.float32), top_p=np.full(B, 0.95, np.float32))
+    cm, cnt = ms.verify_sample(logits, drafts, u, **_on(par))
+    torch.cuda.synchronize()
+    wcm, wn = sp.verify(host(logits), host(drafts), host(u), None, **par)
+    np.testing.assert_array_equal(host(cm), wcm)
+    np.testing.assert_array_equal(host(cnt), wn)
+
+
+def test_binding_refusals(ms):
+    z, u = torch.zeros(4, 16, device="cuda"), torch.zeros(4, device="cuda")
+    i = torch.zeros(4, 3, dtype=torch.int32, device="cuda")
+    for bad in (lambda: ms.sample(z.half(), u), lambda: ms.sample(z[:, ::2], u), lambda: ms.sample(z, u[:3]),
+                lambda: ms.sample(z, u.double()), lambda: ms.sample(z[0], u), lambda: ms.sample(z, u.cpu()),
+                lambda: ms.sample(z, u, top_k=u), lambda: ms.sample(z, u, temperature=u[:2]),
+                lambda: ms.sample(z, u, out=torch.zeros(4, device="cuda")),
+                lambda: ms.verify_sample(z.view(1, 4, 16), i, u.view(1, 4)),
+                lambda: ms.verify_sample(z.view(1, 4, 16), i[:1], u.view(1, 4), draft_probs=z[None])):
+        with pytest.raises(ValueError):
+            bad()
