@@ -20,6 +20,7 @@
 // draw) reads it from there; partial results cross the cluster through
 // distributed shared memory.
 #include <float.h>
+#include <limits.h>
 #include <math.h>
 
 #include "ms_common.cuh"
@@ -34,6 +35,7 @@ constexpr int SP_BINS = 1024;
 constexpr int SP_MAX_V = SP_MAXC * SP_MAX_CHUNK;
 constexpr int SP_FIX = 45;              // fixed point of histogram masses: 2^18 weights of 1 fit 63 bits
 constexpr int SP_LIMB = 15;             // 3 limbs; 2^15 elements x 2^15 fit a 32-bit counter
+constexpr int SP_CAP = 2048;            // candidates of a row that the leader finishes from a list
 static_assert(SP_BINS == 2 * SP_THREADS, "the bin scan gives every thread two bins");
 
 struct SampleArgs {
@@ -149,21 +151,37 @@ struct SpElem<__nv_bfloat16> {
     static __device__ __forceinline__ __nv_bfloat16 ninf() { return __ushort_as_bfloat16(0xff80); }
 };
 
+// Row masses by logit interval, and the candidate lists; never in use together.
 struct SampleSmem {
     double tab[16];
     double wsum[SP_MAXC * SP_WARPS];          // every warp's sum, of every CTA of the cluster
-    double rsum[SP_MAXC * SP_WARPS];          // the same for the residual pass
-    unsigned long long mass[SP_BINS];         // leader: masses pushed by the other CTAs
+    double rsum[SP_MAXC * SP_WARPS];          // the same for the residual
+    double dscan[SP_WARPS];
     unsigned long long scan[SP_WARPS];
-    unsigned long long sel_above;             // broadcast results of a selection round
+    unsigned long long sel_above, sel_total;  // broadcast results of a selection round
+    unsigned long long list_cut;              // broadcast results of a list: composite key of the last token kept,
+    double list_sum;                          // and the sum of the kept weights
+    double wx;
+    union {
+        struct {
+            unsigned long long mass[SP_BINS];   // leader: masses pushed by the other CTAs
+            uint32_t limb[3][SP_BINS];
+        } h;
+        struct {
+            unsigned long long lst[SP_CAP];     // leader: the row's candidates in index order
+            unsigned long long loc[SP_CAP];     // this CTA's candidates; leader, later: the list in descending order
+        } l;
+    };
     uint32_t cnt[SP_BINS];
-    uint32_t limb[3][SP_BINS];
     float cmax[SP_MAXC];
+    uint32_t ccnt[SP_MAXC];
     uint32_t tie[SP_MAXC];
+    float wmax[SP_WARPS];
     uint32_t wcnt[SP_WARPS];
-    uint32_t sel_bin, sel_cnt;
+    uint32_t sel_bin, sel_cnt, sel_cabove;
     uint32_t cut_idx;                         // broadcast: index of the last tied token kept
     int last;
+    uint32_t keep;
 };
 
 // Where a CTA's part of the row sits: element i (row index begin + i) is
@@ -172,124 +190,36 @@ template <typename TL>
 struct SpChunk {
     TL* buf;
     int mis, n, nvec, begin;
-};
-
-// A selected set: logits >= lcut whose composite key (order, lower index first)
-// is at least `cut`.
-struct SpCut {
-    float lcut;
-    unsigned long long cut;
-};
-__device__ __forceinline__ unsigned long long composite(uint32_t key, int idx) {
-    return (static_cast<unsigned long long>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(idx));
-}
-
-// One selection round trip: histogram of the cluster's elements with keys in
-// [klo, khi] over up to SP_BINS equal key intervals, counts always and masses
-// (fixed point) when MASS; the leader finds the first interval, from the
-// largest keys down, where `above` + the running total reaches the target.
-// Repeats on that interval until it is a single key.  Every thread of every
-// CTA of the cluster calls this with the same arguments.
-template <typename TL, bool MASS>
-__device__ void radix_select(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, uint32_t klo,
-                             uint32_t khi, float lcut, double md, double c, double target, uint32_t& key_out,
-                             unsigned long long& above_out, uint32_t& cnt_out) {
-    constexpr int VEC = SpElem<TL>::VEC, KSH = SpElem<TL>::KSH;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned long long above = 0;
-    const uint4* bv = reinterpret_cast<const uint4*>(ck.buf);
-    while (true) {
-        int sh = 0;
-        while (((khi - klo) >> sh) >= SP_BINS) ++sh;
-        for (int i = tid; i < SP_BINS; i += SP_THREADS) {
-            sm.cnt[i] = 0;
-            if (MASS) {
-                sm.limb[0][i] = sm.limb[1][i] = sm.limb[2][i] = 0;
-                sm.mass[i] = 0;
-            }
-        }
-        if (tid == 0) sm.last = 0;
-        cluster_sync_all();   // the leader's tables are clear before anyone adds to them
-        for (int q = tid; q < ck.nvec; q += SP_THREADS) {
-            float v[VEC];
-            SpElem<TL>::unpack(bv[q], v);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                if (!(v[e] >= lcut)) continue;
-                const uint32_t key = order_key(v[e]) >> KSH;
-                if (key < klo || key > khi) continue;
-                const uint32_t bin = (khi - key) >> sh;
-                atomicAdd(&sm.cnt[bin], 1u);
-                if (MASS) {
-                    const double w = exp2_64((bits_to_f64(__float_as_uint(v[e])) - md) * c, sm.tab);
-                    const unsigned long long W = __double2ull_rn(w * static_cast<double>(1ull << SP_FIX));
-                    atomicAdd(&sm.limb[0][bin], static_cast<uint32_t>(W) & ((1u << SP_LIMB) - 1));
-                    atomicAdd(&sm.limb[1][bin], static_cast<uint32_t>(W >> SP_LIMB) & ((1u << SP_LIMB) - 1));
-                    atomicAdd(&sm.limb[2][bin], static_cast<uint32_t>(W >> (2 * SP_LIMB)));
-                }
-            }
-        }
-        __syncthreads();
-        if (rank != 0) {
-            for (int i = tid; i < SP_BINS; i += SP_THREADS) {
-                if (sm.cnt[i] == 0) continue;
-                if (MASS)
-                    red_cluster_u64(&sm.mass[i], 0,
-                                    sm.limb[0][i] + (static_cast<unsigned long long>(sm.limb[1][i]) << SP_LIMB) +
-                                        (static_cast<unsigned long long>(sm.limb[2][i]) << (2 * SP_LIMB)));
-                red_cluster_u32(&sm.cnt[i], 0, sm.cnt[i]);
-            }
-        }
-        cluster_sync_all();
-        if (rank == 0) {
-            unsigned long long v[2];
-            uint32_t n[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int i = 2 * tid + j;
-                n[j] = sm.cnt[i];
-                v[j] = n[j];
-                if (MASS)
-                    v[j] = sm.mass[i] + sm.limb[0][i] + (static_cast<unsigned long long>(sm.limb[1][i]) << SP_LIMB) +
-                           (static_cast<unsigned long long>(sm.limb[2][i]) << (2 * SP_LIMB));
-                if (n[j]) atomicMax(&sm.last, i);
-            }
-            const unsigned long long own = v[0] + v[1];
-            const unsigned long long inc = warp_scan(own, lane);
-            if (lane == 31) sm.scan[warp] = inc;
-            __syncthreads();
-            unsigned long long ex = above + inc - own;
-            for (int w = 0; w < warp; ++w) ex += sm.scan[w];
-            unsigned long long tot = above;
-            for (int w = 0; w < SP_WARPS; ++w) tot += sm.scan[w];
-            // the last occupied interval where rounding left the target above the total
-            const bool never = static_cast<double>(tot) < target;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const bool hit = never ? 2 * tid + j == sm.last
-                                       : n[j] && static_cast<double>(ex) < target &&
-                                             static_cast<double>(ex + v[j]) >= target;
-                if (hit)
-                    for (uint32_t r = 0; r < C; ++r) {
-                        st_cluster_s32(&sm.sel_bin, r, 2 * tid + j);
-                        st_cluster_s32(&sm.sel_cnt, r, static_cast<int>(n[j]));
-                        st_cluster_u64(&sm.sel_above, r, ex);
-                    }
-                ex += v[j];
-            }
-        }
-        cluster_sync_all();
-        above = sm.sel_above;
-        khi -= sm.sel_bin << sh;
-        const uint32_t span = (1u << sh) - 1;
-        klo = khi - klo > span ? khi - span : klo;
-        if (sh == 0) {
-            key_out = khi;
-            above_out = above;
-            cnt_out = sm.sel_cnt;
-            return;
-        }
+    __device__ __forceinline__ int index(int vec, int e) const { return begin + vec * SpElem<TL>::VEC + e - mis; }
+    __device__ __forceinline__ void load(int vec, float (&v)[SpElem<TL>::VEC]) const {
+        SpElem<TL>::unpack(reinterpret_cast<const uint4*>(buf)[vec], v);
     }
+};
+
+// The row's weights: w(l) = 2^((l - max) c), c = log2(e) / T.
+struct SpScale {
+    float m;        // max l
+    double md, c;
+    const double* tab;
+    __device__ __forceinline__ double weight(float l) const {
+        return exp2_64((bits_to_f64(__float_as_uint(l)) - md) * c, tab);
+    }
+};
+
+// A kept set: logits above tau, and those equal to it up to index icut.
+struct SpCut {
+    float tau;
+    int icut;
+    __device__ __forceinline__ bool keeps(float l, int idx) const { return l > tau || (l == tau && idx <= icut); }
+};
+
+// Tokens in descending order: (logit, lower index first) as one integer.
+__device__ __forceinline__ unsigned long long composite(float l, int idx) {
+    return (static_cast<unsigned long long>(order_key(l)) << 32) | (0xffffffffu - static_cast<uint32_t>(idx));
+}
+__device__ __forceinline__ float composite_value(unsigned long long k) { return key_value(static_cast<uint32_t>(k >> 32)); }
+__device__ __forceinline__ int composite_index(unsigned long long k) {
+    return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
 }
 
 // Index range of a warp's part of the chunk, in 16-byte vectors: contiguous,
@@ -300,36 +230,521 @@ __device__ __forceinline__ void warp_segment(int nvec, int warp, int& q0, int& q
     q1 = min(nvec, q0 + per);
 }
 
-// The weight of one element under a cut, and of the residual max(w - q S, 0)
-// where the row's draft probabilities are given.
+// ---------------------------------------------------------------- selection
+// Logit intervals of equal width below the maximum; the last one takes the rest.
+struct SpBins {
+    float m, s;
+    __device__ __forceinline__ uint32_t of(float l) const {
+        return min(static_cast<uint32_t>((m - l) * s), static_cast<uint32_t>(SP_BINS - 1));   // NaN (inf - inf): 0
+    }
+};
+
+struct SpBin {
+    uint32_t b, cnt, cabove;            // the interval, its tokens, the tokens above it
+    unsigned long long above, total;    // masses (or counts) above it, and of the row
+};
+
+// The leader's part of a selection round: merges the tables, scans them from
+// the top and broadcasts the first interval where `above` + the running total
+// reaches the target (`frac` of the round's total where target < 0).
+template <bool MASS>
+__device__ void select_bin(SampleSmem& sm, uint32_t C, unsigned long long above, uint32_t cabove, double target,
+                           double frac) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned long long v[2];
+    uint32_t n[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = 2 * tid + j;
+        n[j] = sm.cnt[i];
+        v[j] = n[j];
+        if (MASS)
+            v[j] = sm.h.mass[i] + sm.h.limb[0][i] + (static_cast<unsigned long long>(sm.h.limb[1][i]) << SP_LIMB) +
+                   (static_cast<unsigned long long>(sm.h.limb[2][i]) << (2 * SP_LIMB));
+        if (n[j]) atomicMax(&sm.last, i);
+    }
+    const unsigned long long own = v[0] + v[1];
+    const unsigned long long inc = warp_scan(own, lane);
+    const uint32_t cown = n[0] + n[1];
+    const uint32_t cinc = warp_scan(cown, lane);
+    if (lane == 31) {
+        sm.scan[warp] = inc;
+        sm.wcnt[warp] = cinc;
+    }
+    __syncthreads();
+    unsigned long long ex = above + inc - own, tot = above;
+    uint32_t cex = cabove + cinc - cown;
+    for (int w = 0; w < SP_WARPS; ++w) {
+        if (w < warp) {
+            ex += sm.scan[w];
+            cex += sm.wcnt[w];
+        }
+        tot += sm.scan[w];
+    }
+    if (target < 0.0) target = fmax(frac * static_cast<double>(tot), 0.5);
+    // the last occupied interval where rounding left the target above the total
+    const bool never = static_cast<double>(tot) < target;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const bool hit = never ? 2 * tid + j == sm.last
+                               : n[j] && static_cast<double>(ex) < target && static_cast<double>(ex + v[j]) >= target;
+        if (hit)
+            for (uint32_t r = 0; r < C; ++r) {
+                st_cluster_s32(&sm.sel_bin, r, 2 * tid + j);
+                st_cluster_s32(&sm.sel_cnt, r, static_cast<int>(n[j]));
+                st_cluster_s32(&sm.sel_cabove, r, static_cast<int>(cex));
+                st_cluster_u64(&sm.sel_above, r, ex);
+                st_cluster_u64(&sm.sel_total, r, tot);
+            }
+        ex += v[j];
+        cex += n[j];
+    }
+}
+
+// One selection round over the cluster's part of the row: a histogram of the
+// elements that bin_of() accepts (counts always, fixed-point masses when MASS),
+// merged and scanned by the leader.  Elements of the last interval are summed
+// in registers when LAST: it takes the bulk of a peaked row.
+template <typename TL, bool MASS, bool LAST, typename F>
+__device__ SpBin select_round(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
+                              unsigned long long above, uint32_t cabove, double target, double frac, F bin_of) {
+    constexpr int VEC = SpElem<TL>::VEC;
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int i = tid; i < SP_BINS; i += SP_THREADS) {
+        sm.cnt[i] = 0;
+        if (MASS) {
+            sm.h.limb[0][i] = sm.h.limb[1][i] = sm.h.limb[2][i] = 0;
+            sm.h.mass[i] = 0;
+        }
+    }
+    if (tid == 0) sm.last = 0;
+    cluster_sync_all();   // the leader's tables are clear before anyone adds to them
+    uint32_t rest_n = 0;
+    unsigned long long rest = 0;
+    for (int q = tid; q < ck.nvec; q += SP_THREADS) {
+        float v[VEC];
+        ck.load(q, v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            uint32_t bin;
+            if (!bin_of(v[e], bin)) continue;
+            unsigned long long W = 0;
+            if (MASS) {
+                // adding 2^7 leaves the weight as an integer of 2^-45 in the low mantissa bits
+                const double z = sc.weight(v[e]) + 128.0;
+                W = static_cast<unsigned long long>(__double_as_longlong(z)) & 0xfffffffffffffull;
+            }
+            if (LAST && bin == SP_BINS - 1) {
+                ++rest_n;
+                rest += W;
+                continue;
+            }
+            atomicAdd(&sm.cnt[bin], 1u);
+            if (MASS) {
+                atomicAdd(&sm.h.limb[0][bin], static_cast<uint32_t>(W) & ((1u << SP_LIMB) - 1));
+                atomicAdd(&sm.h.limb[1][bin], static_cast<uint32_t>(W >> SP_LIMB) & ((1u << SP_LIMB) - 1));
+                atomicAdd(&sm.h.limb[2][bin], static_cast<uint32_t>(W >> (2 * SP_LIMB)));
+            }
+        }
+    }
+    if (LAST) {
+        rest_n = __reduce_add_sync(0xffffffffu, rest_n);
+        if (MASS) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        }
+        if (lane == 0 && rest_n) {
+            atomicAdd(&sm.cnt[SP_BINS - 1], rest_n);
+            if (MASS) {
+                atomicAdd(&sm.h.limb[0][SP_BINS - 1], static_cast<uint32_t>(rest) & ((1u << SP_LIMB) - 1));
+                atomicAdd(&sm.h.limb[1][SP_BINS - 1], static_cast<uint32_t>(rest >> SP_LIMB) & ((1u << SP_LIMB) - 1));
+                atomicAdd(&sm.h.limb[2][SP_BINS - 1], static_cast<uint32_t>(rest >> (2 * SP_LIMB)));
+            }
+        }
+    }
+    __syncthreads();
+    if (rank != 0) {
+        for (int i = tid; i < SP_BINS; i += SP_THREADS) {
+            if (sm.cnt[i] == 0) continue;
+            if (MASS)
+                red_cluster_u64(&sm.h.mass[i], 0,
+                                sm.h.limb[0][i] + (static_cast<unsigned long long>(sm.h.limb[1][i]) << SP_LIMB) +
+                                    (static_cast<unsigned long long>(sm.h.limb[2][i]) << (2 * SP_LIMB)));
+            red_cluster_u32(&sm.cnt[i], 0, sm.cnt[i]);
+        }
+    }
+    cluster_sync_all();
+    if (rank == 0) select_bin<MASS>(sm, C, above, cabove, target, frac);
+    cluster_sync_all();
+    return SpBin{sm.sel_bin, sm.sel_cnt, sm.sel_cabove, sm.sel_above, sm.sel_total};
+}
+
+// First round: intervals of the logit itself over the 24 binary orders of
+// magnitude below the largest weight, or down to `lo` where that is nearer.
+__device__ __forceinline__ SpBins first_bins(const SpScale& sc, float lo) {
+    const float width = fminf(sc.m - lo, static_cast<float>(24.0 / sc.c));
+    return SpBins{sc.m, width > 0.f && width < 1e30f ? static_cast<float>(SP_BINS - 1) / width : 0.f};
+}
+
+template <typename TL, bool MASS>
+__device__ SpBin select_first(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
+                              float lo, double target, double frac) {
+    const SpBins bins = first_bins(sc, lo);
+    return select_round<TL, MASS, true>(sm, ck, sc, rank, C, 0ull, 0u, target, frac, [&](float l, uint32_t& bin) {
+        bin = bins.of(l);
+        return l >= lo;
+    });
+}
+
+// Later rounds: the ordered keys of one interval, SP_BINS ranges at a time, down
+// to a single key.  Returns that key; `at` becomes its entry.
+template <typename TL, bool MASS>
+__device__ uint32_t select_key(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
+                               float lo, double target, SpBin& at) {
+    constexpr int KSH = SpElem<TL>::KSH;
+    const SpBins bins = first_bins(sc, lo);
+    const uint32_t b0 = at.b;
+    // bounds of the interval's logits, widened by more than the rounding of SpBins::of
+    float top = sc.m, bot = lo;
+    if (bins.s > 0.f) {
+        const float slack = fabsf(sc.m) * 3e-7f;
+        if (b0 > 0) top = fminf(sc.m, sc.m - static_cast<float>(b0) / bins.s * (1.f - 1e-6f) + slack);
+        if (b0 < SP_BINS - 1) bot = fmaxf(lo, sc.m - static_cast<float>(b0 + 1) / bins.s * (1.f + 1e-6f) - slack);
+    }
+    uint32_t khi = order_key(top) >> KSH, klo = order_key(bot) >> KSH;
+    const unsigned long long total = at.total;
+    while (khi > klo) {
+        int sh = 0;
+        while (((khi - klo) >> sh) >= SP_BINS) ++sh;
+        at = select_round<TL, MASS, false>(sm, ck, sc, rank, C, at.above, at.cabove, target, 0.0,
+                                           [&](float l, uint32_t& bin) {
+                                               const uint32_t key = order_key(l) >> KSH;
+                                               bin = (khi - key) >> sh;
+                                               return l >= lo && key >= klo && key <= khi && bins.of(l) == b0;
+                                           });
+        khi -= at.b << sh;
+        const uint32_t span = (1u << sh) - 1;
+        klo = khi - klo > span ? khi - span : klo;
+    }
+    at.total = total;
+    return khi;
+}
+
+// The logit that a key stands for.
 template <typename TL>
-__device__ __forceinline__ double kept_weight(float l, int idx, const SpCut& cut, double md, double c, int skip,
-                                              const float* q, double S, const double* tab) {
-    if (!(l >= cut.lcut) || idx == skip) return 0.0;
-    if (composite(order_key(l) >> SpElem<TL>::KSH, idx) < cut.cut) return 0.0;
-    const double w = exp2_64((bits_to_f64(__float_as_uint(l)) - md) * c, tab);
-    if (!q) return w;
-    const double r = w - static_cast<double>(__ldg(q + idx)) * S;
-    return r > 0.0 ? r : 0.0;
+__device__ __forceinline__ float key_logit(uint32_t key) {
+    constexpr int KSH = SpElem<TL>::KSH;
+    return key_value(KSH ? (key << KSH) | ((key >> 15) ? 0u : 0xffffu) : key);
+}
+
+// This CTA's elements that keep() accepts as composite keys in sm.l.loc, in
+// index order, and the count of every CTA in sm.ccnt.  Returns the cluster's
+// count; where it exceeds SP_CAP the lists are not complete.
+template <typename TL, typename F>
+__device__ uint32_t gather(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, F keep) {
+    constexpr int VEC = SpElem<TL>::VEC;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int q0, q1;
+    warp_segment(ck.nvec, warp, q0, q1);
+    uint32_t n = 0;
+    for (int q = q0 + lane; q < q1; q += 32) {
+        float v[VEC];
+        ck.load(q, v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) n += keep(v[e]) ? 1u : 0u;
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) sm.wcnt[warp] = n;
+    __syncthreads();
+    uint32_t at = 0, tot = 0;
+#pragma unroll
+    for (int w = 0; w < SP_WARPS; ++w) {
+        const uint32_t x = sm.wcnt[w];
+        if (w < warp) at += x;
+        tot += x;
+    }
+    if (tid < static_cast<int>(C)) st_cluster_s32(&sm.ccnt[rank], tid, static_cast<int>(tot));
+    if (tot <= SP_CAP && n > 0) {
+        for (int v0 = q0; v0 < q1; v0 += 32) {
+            uint32_t mask = 0;
+            float v[VEC];
+            if (v0 + lane < q1) {
+                ck.load(v0 + lane, v);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) mask |= (keep(v[e]) ? 1u : 0u) << e;
+            }
+            if (!__any_sync(0xffffffffu, mask)) continue;
+            const uint32_t mine = __popc(mask);
+            const uint32_t in = warp_scan(mine, lane);
+            uint32_t w = at + in - mine;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (mask & (1u << e)) sm.l.loc[w++] = composite(v[e], ck.index(v0 + lane, e));
+            at += __shfl_sync(0xffffffffu, in, 31);
+        }
+    }
+    cluster_sync_all();
+    uint32_t all = 0;
+    for (uint32_t r = 0; r < C; ++r) all += sm.ccnt[r];
+    return all;
+}
+
+// A lower bound of the k-th largest logit: the k-th largest of the threads'
+// maxima (each of k threads holds an element at least that large), to within
+// an interval.  -inf where fewer than k threads hold an element above lo.
+__device__ float kth_bound(SampleSmem& sm, const SpScale& sc, uint32_t C, float lo, float mine, uint32_t k) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const SpBins bins = first_bins(sc, lo);
+    if (mine >= lo) atomicAdd(&sm.cnt[bins.of(mine)], 1u);   // cleared before the first cluster barrier
+    cluster_sync_all();
+    uint32_t n[2] = {0, 0};
+#pragma unroll 8
+    for (uint32_t r = 0; r < C; ++r) {
+        uint32_t x, y;
+        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(sp_mapa(&sm.cnt[2 * tid], r)) : "memory");
+        n[0] += x;
+        n[1] += y;
+    }
+    if (tid == 0) sm.last = SP_BINS;
+    const uint32_t own = n[0] + n[1];
+    const uint32_t inc = warp_scan(own, lane);
+    if (lane == 31) sm.wcnt[warp] = inc;
+    __syncthreads();
+    uint32_t ex = inc - own;
+    for (int w = 0; w < warp; ++w) ex += sm.wcnt[w];
+    if (ex < k && ex + own >= k) sm.last = ex + n[0] >= k ? 2 * tid : 2 * tid + 1;
+    __syncthreads();
+    const int b = sm.last;
+    __syncthreads();   // wcnt and last are free again
+    if (b >= SP_BINS - 1 || !(bins.s > 0.f)) return lo;
+    return fmaxf(lo, sc.m - static_cast<float>(b + 1) / bins.s * (1.f + 1e-6f) - fabsf(sc.m) * 3e-7f);
+}
+
+// ---------------------------------------------------------------- the draw from a list (leader)
+// Sums over per-thread runs: start of this thread's run and the total.  A
+// thread's end is the next one's start exactly.
+__device__ __forceinline__ void block_runs(SampleSmem& sm, double own, int nwarps, double& start, double& end,
+                                           double& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const double inc = warp_scan(own, lane);
+    double prev = __shfl_up_sync(0xffffffffu, inc, 1);
+    if (lane == 0) prev = 0.0;
+    __syncthreads();
+    if (lane == 31) sm.dscan[warp] = inc;
+    __syncthreads();
+    double base = 0.0, sum = 0.0;
+    for (int w = 0; w < nwarps; ++w) {
+        if (w == warp) base = sum;
+        sum += sm.dscan[w];
+    }
+    start = base + prev;
+    end = base + inc;
+    total = sum;
+}
+
+// Descending order of n composite keys from lst into srt.
+__device__ void sort_list(SampleSmem& sm, const unsigned long long* lst, unsigned long long* srt, int n) {
+    const int tid = threadIdx.x;
+    if (n <= 128) {   // each key's rank by counting, four threads a key
+        uint32_t* rk = sm.cnt;
+        for (int i = tid; i < 128; i += SP_THREADS) rk[i] = 0;
+        __syncthreads();
+        const int i = tid & 127, part = tid >> 7;
+        if (i < n) {
+            const unsigned long long k = lst[i];
+            const int per = (n + 3) / 4;
+            uint32_t r = 0;
+#pragma unroll 4
+            for (int j = part * per; j < min(n, part * per + per); ++j) r += lst[j] > k;
+            atomicAdd(&rk[i], r);
+        }
+        __syncthreads();
+        if (tid < n) srt[rk[tid]] = lst[tid];
+        __syncthreads();
+        return;
+    }
+    int p2 = 256;
+    while (p2 < n) p2 *= 2;
+    for (int i = tid; i < p2; i += SP_THREADS) srt[i] = i < n ? lst[i] : 0ull;
+    __syncthreads();
+    for (int size = 2; size <= p2; size *= 2)
+        for (int step = size / 2; step > 0; step /= 2) {
+            for (int i = tid; i < p2 / 2; i += SP_THREADS) {
+                const int a = 2 * i - (i & (step - 1)), b = a + step;
+                const unsigned long long x = srt[a], y = srt[b];
+                const bool desc = (a & size) == 0;
+                if ((x < y) == desc) {
+                    srt[a] = y;
+                    srt[b] = x;
+                }
+            }
+            __syncthreads();
+        }
+}
+
+constexpr int SP_PER = SP_CAP / SP_THREADS;
+
+// Index of the entry of the list where the running sum of w (this thread's
+// run starts at `start`) passes the target, in the one thread it falls to; -1
+// elsewhere.
+__device__ __forceinline__ int run_hit(const double (&w)[SP_PER], double start, double end, double target) {
+    if (!(start <= target && target < end)) return -1;
+    int at = -1;
+    double acc = start;
+#pragma unroll
+    for (int e = 0; e < SP_PER; ++e) {
+        if (w[e] > 0.0 && (at < 0 || acc <= target)) at = e;   // the first that passes, else the last with weight
+        acc += w[e];
+    }
+    return at;
+}
+
+struct SpRow {
+    bool by_k, by_p;
+    int k;
+    double p;
+    int x;              // the draft, or -1
+    bool has_draft;
+    const float* q;     // its distribution, or NULL
+    double ua, us;
+};
+
+// The leader's end of a row whose kept tokens all lie in the list lst[0..n):
+// filters, acceptance of the draft, the draw.  S_all: the row's sum before
+// top-p, or negative where the list is the whole row.
+template <bool VERIFY>
+__device__ void draw_from_list(SampleSmem& sm, int n, const SpScale& sc, const SpRow& r, double S_all, int32_t* token,
+                               int32_t* accepted) {
+    const int tid = threadIdx.x;
+    const unsigned long long* lst = sm.l.lst;
+    unsigned long long* srt = sm.l.loc;
+    const int per = (n + SP_THREADS - 1) / SP_THREADS;
+    const int nwarps = min(SP_WARPS, (n + 32 * per - 1) / (32 * per));
+    int nk = r.by_k ? min(r.k, n) : n;
+    unsigned long long cut = 0;
+    if (nk < n || r.by_p) {
+        sort_list(sm, lst, srt, n);
+        if (r.by_p) {
+            if (tid == 0) sm.keep = nk;
+            double w[SP_PER], own = 0.0, start, end, total;
+#pragma unroll
+            for (int e = 0; e < SP_PER; ++e) {
+                const int j = tid * per + e;
+                w[e] = e < per && j < nk ? sc.weight(composite_value(srt[j])) : 0.0;
+                own += w[e];
+            }
+            block_runs(sm, own, nwarps, start, end, total);
+            const double target = fmax(r.p * (r.by_k || S_all < 0.0 ? total : S_all), 1e-9);
+            // the prefix ends with the first token at which the running sum reaches the target
+            if (start < target && end >= target) {
+                double acc = start;
+                int at = -1;
+#pragma unroll
+                for (int e = 0; e < SP_PER; ++e) {
+                    if (w[e] > 0.0 && (at < 0 || acc < target)) at = e;
+                    acc += w[e];
+                }
+                sm.keep = tid * per + at + 1;
+            }
+            __syncthreads();
+            nk = sm.keep;
+        }
+        cut = srt[nk - 1];
+    }
+    if (tid == 0) sm.wx = 0.0;
+    __syncthreads();
+    double w[SP_PER], own = 0.0, start, end, total;
+#pragma unroll
+    for (int e = 0; e < SP_PER; ++e) {
+        const int j = tid * per + e;
+        w[e] = 0.0;
+        if (e < per && j < n && lst[j] >= cut) {
+            w[e] = sc.weight(composite_value(lst[j]));
+            if (VERIFY && r.has_draft && composite_index(lst[j]) == r.x) {
+                sm.wx = w[e];
+                if (!r.q) w[e] = 0.0;   // a certain draft leaves the others
+            }
+        }
+        own += w[e];
+    }
+    block_runs(sm, own, nwarps, start, end, total);
+    double S = total;
+    if (VERIFY && r.has_draft) {
+        const double wx = sm.wx;
+        if (!r.q) S = total + wx;
+        const double qx = r.q ? (r.x >= 0 ? static_cast<double>(__ldg(r.q + r.x)) : 0.0) : 1.0;
+        if (wx > 0.0 && r.ua * qx * S < wx) {
+            if (tid == 0) {
+                *token = r.x;
+                *accepted = 1;
+            }
+            return;
+        }
+        if (r.q) {
+            double rw[SP_PER], rown = 0.0, rs, re, rt;
+#pragma unroll
+            for (int e = 0; e < SP_PER; ++e) {
+                rw[e] = 0.0;
+                if (w[e] > 0.0)
+                    rw[e] = fmax(0.0, w[e] - static_cast<double>(__ldg(r.q + composite_index(lst[tid * per + e]))) * S);
+                rown += rw[e];
+            }
+            block_runs(sm, rown, nwarps, rs, re, rt);
+            if (rt > 0.0) {
+#pragma unroll
+                for (int e = 0; e < SP_PER; ++e) w[e] = rw[e];
+                start = rs;
+                end = re;
+                total = rt;
+            }
+        }
+    }
+    if (tid == 0) {
+        sm.list_cut = cut;
+        sm.list_sum = S;
+    }
+    if (!(total > 0.0)) {   // the draft is the only token kept
+        if (tid == 0) {
+            *token = r.x;
+            if (VERIFY) *accepted = 0;
+        }
+        return;
+    }
+    const int e = run_hit(w, start, end, r.us * total);
+    if (e >= 0) {
+        *token = composite_index(lst[tid * per + e]);
+        if (VERIFY) *accepted = 0;
+    }
+}
+
+// ---------------------------------------------------------------- the draw from the whole row
+// A warp's kept weights in index order; with q, the residual max(w - q S, 0).
+template <typename TL>
+__device__ __forceinline__ double kept_weight(float l, int idx, const SpCut& cut, const SpScale& sc, int skip,
+                                              const float* q, double S) {
+    double w = 0.0;
+    if (cut.keeps(l, idx) && idx != skip) {
+        w = sc.weight(l);
+        if (q) w = fmax(0.0, w - static_cast<double>(__ldg(q + idx)) * S);
+    }
+    return w;
 }
 
 // Sum of every warp's kept weights into sums[cta][warp] of every CTA (one
 // cluster barrier).
 template <typename TL>
-__device__ void segment_sums(SampleSmem& sm, double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C,
-                             const SpCut& cut, double md, double c, int skip, const float* q, double S) {
+__device__ void segment_sums(double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, const SpCut& cut,
+                             const SpScale& sc, int skip, const float* q, double S) {
     constexpr int VEC = SpElem<TL>::VEC;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint4* bv = reinterpret_cast<const uint4*>(ck.buf);
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
     double s = 0.0;
     for (int v0 = q0 + lane; v0 < q1; v0 += 32) {
         float v[VEC];
-        SpElem<TL>::unpack(bv[v0], v);
+        ck.load(v0, v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            s += kept_weight<TL>(v[e], ck.begin + v0 * VEC + e - ck.mis, cut, md, c, skip, q, S, sm.tab);
+        for (int e = 0; e < VEC; ++e) s += kept_weight<TL>(v[e], ck.index(v0, e), cut, sc, skip, q, S);
     }
     s = warp_sum_f64(s);
     if (lane < static_cast<int>(C)) st_cluster_f64(&sums[rank * SP_WARPS + warp], lane, s);
@@ -343,11 +758,11 @@ __device__ double table_sum(const double* sums, uint32_t C, int lane) {
     return warp_sum_f64(s);
 }
 
-// The draw: the first index whose cumulative weight exceeds u times the total.
-// Returns the token in lane 0 of the warp that owns it, -1 elsewhere.
+// The first index whose cumulative weight exceeds u times the total.  Returns
+// the token in the warp that owns it, -1 elsewhere.
 template <typename TL>
-__device__ int draw_token(SampleSmem& sm, const double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C,
-                          const SpCut& cut, double md, double c, int skip, const float* q, double S, double u) {
+__device__ int draw_token(const double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, const SpCut& cut,
+                          const SpScale& sc, int skip, const float* q, double S, double u) {
     constexpr int VEC = SpElem<TL>::VEC;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nseg = static_cast<int>(C) * SP_WARPS;
@@ -385,7 +800,6 @@ __device__ int draw_token(SampleSmem& sm, const double* sums, const SpChunk<TL>&
     seg = __shfl_sync(0xffffffffu, seg, src);
     base = __shfl_sync(0xffffffffu, seg_base, src);
     if (seg != static_cast<int>(rank) * SP_WARPS + warp) return -1;
-    const uint4* bv = reinterpret_cast<const uint4*>(ck.buf);
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
     int last = -1;
@@ -397,12 +811,12 @@ __device__ int draw_token(SampleSmem& sm, const double* sums, const SpChunk<TL>&
         for (int e = 0; e < VEC; ++e) w[e] = 0.0;
         if (vq < q1) {
             float v[VEC];
-            SpElem<TL>::unpack(bv[vq], v);
+            ck.load(vq, v);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                w[e] = kept_weight<TL>(v[e], ck.begin + vq * VEC + e - ck.mis, cut, md, c, skip, q, S, sm.tab);
+                w[e] = kept_weight<TL>(v[e], ck.index(vq, e), cut, sc, skip, q, S);
                 s += w[e];
-                if (w[e] > 0.0) mine = ck.begin + vq * VEC + e - ck.mis;
+                if (w[e] > 0.0) mine = ck.index(vq, e);
             }
         }
         const double in = warp_scan(s, lane);
@@ -410,13 +824,14 @@ __device__ int draw_token(SampleSmem& sm, const double* sums, const SpChunk<TL>&
         if (pass) {
             int tok = mine;
             double acc = base + in - s;
+            bool found = false;
 #pragma unroll
-            for (int e = VEC - 1; e >= 0; --e) {
-                // from the back: the lowest element whose running sum exceeds the target stays
-                double before = acc;
-#pragma unroll
-                for (int f = 0; f < e; ++f) before += w[f];
-                if (w[e] > 0.0 && before + w[e] > target) tok = ck.begin + vq * VEC + e - ck.mis;
+            for (int e = 0; e < VEC; ++e) {
+                acc += w[e];
+                if (!found && w[e] > 0.0 && acc > target) {
+                    tok = ck.index(vq, e);
+                    found = true;
+                }
             }
             return __shfl_sync(0xffffffffu, tok, __ffs(pass) - 1);
         }
@@ -427,15 +842,68 @@ __device__ int draw_token(SampleSmem& sm, const double* sums, const SpChunk<TL>&
     return last;
 }
 
+// Index of the keep-th token with logit tau, in index order, of `ties` in the
+// row (two cluster barriers).
+template <typename TL>
+__device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float tau, uint32_t keep) {
+    constexpr int VEC = SpElem<TL>::VEC;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int q0, q1;
+    warp_segment(ck.nvec, warp, q0, q1);
+    uint32_t n = 0;
+    for (int q = q0 + lane; q < q1; q += 32) {
+        float v[VEC];
+        ck.load(q, v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) n += v[e] == tau ? 1u : 0u;
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) sm.wcnt[warp] = n;
+    __syncthreads();
+    uint32_t tot = 0, before = 0;
+    for (int w = 0; w < SP_WARPS; ++w) {
+        if (w < warp) before += sm.wcnt[w];
+        tot += sm.wcnt[w];
+    }
+    if (tid < static_cast<int>(C)) st_cluster_s32(&sm.tie[rank], tid, static_cast<int>(tot));
+    cluster_sync_all();
+    for (uint32_t r = 0; r < rank; ++r) before += sm.tie[r];
+    if (keep > before && keep <= before + n) {
+        uint32_t left = keep - before;   // 1-based
+        for (int v0 = q0; v0 < q1; v0 += 32) {
+            uint32_t mask = 0;
+            if (v0 + lane < q1) {
+                float v[VEC];
+                ck.load(v0 + lane, v);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) mask |= (v[e] == tau ? 1u : 0u) << e;
+            }
+            const uint32_t mine = __popc(mask);
+            const uint32_t in = warp_scan(mine, lane);
+            if (in >= left && in - mine < left) {
+                uint32_t skip = left - (in - mine) - 1;
+                while (skip--) mask &= mask - 1;
+                for (uint32_t r = 0; r < C; ++r) st_cluster_s32(&sm.cut_idx, r, ck.index(v0 + lane, __ffs(mask) - 1));
+            }
+            const uint32_t t = __shfl_sync(0xffffffffu, in, 31);
+            if (t >= left) break;
+            left -= t;
+        }
+    }
+    cluster_sync_all();
+    return static_cast<int>(sm.cut_idx);
+}
+
 template <typename TL, bool VERIFY>
-__global__ void __launch_bounds__(SP_THREADS) sample_kernel(const SampleArgs a) {
-    constexpr int VEC = SpElem<TL>::VEC, KSH = SpElem<TL>::KSH;
+__global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs a) {
+    constexpr int VEC = SpElem<TL>::VEC;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ SampleSmem sm;
     const uint32_t rank = cluster_rank(), C = a.cluster;
     const int row = blockIdx.x / a.cluster;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < 16) sm.tab[tid] = exp2(static_cast<double>(tid) / 16.0);
+    for (int i = tid; i < SP_BINS; i += SP_THREADS) sm.cnt[i] = 0;
     grid_dep_wait();
     grid_dep_launch();
 
@@ -448,62 +916,81 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(const SampleArgs a) 
     const TL* g = rowp + ck.begin;
     ck.mis = static_cast<int>((reinterpret_cast<uintptr_t>(g) & 15u) / sizeof(TL));
     ck.nvec = ck.n > 0 ? (ck.mis + ck.n + VEC - 1) / VEC : 0;
-    float m = -INFINITY;
-    for (int q = tid; q < ck.nvec; q += SP_THREADS) {
-        const int s0 = q * VEC;
-        uint4 r;
-        if (s0 >= ck.mis && s0 + VEC <= ck.mis + ck.n) {
-            r = __ldg(reinterpret_cast<const uint4*>(g + (s0 - ck.mis)));
-        } else {
-            TL t[VEC];
+    float mine = -INFINITY;
+    for (int q0 = tid; q0 < ck.nvec; q0 += 4 * SP_THREADS) {
+        uint4 r[4];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                t[e] = s0 + e >= ck.mis && s0 + e < ck.mis + ck.n ? g[s0 + e - ck.mis] : SpElem<TL>::ninf();
-            memcpy(&r, t, 16);
+        for (int j = 0; j < 4; ++j) {
+            const int s0 = (q0 + j * SP_THREADS) * VEC;
+            if (s0 >= ck.mis && s0 + VEC <= ck.mis + ck.n)
+                r[j] = __ldg(reinterpret_cast<const uint4*>(g + (s0 - ck.mis)));
         }
-        reinterpret_cast<uint4*>(ck.buf)[q] = r;
-        float v[VEC];
-        SpElem<TL>::unpack(r, v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) m = fmaxf(m, v[e]);   // a NaN operand is ignored
+        for (int j = 0; j < 4; ++j) {
+            const int q = q0 + j * SP_THREADS, s0 = q * VEC;
+            if (q >= ck.nvec) break;
+            if (!(s0 >= ck.mis && s0 + VEC <= ck.mis + ck.n)) {   // a ragged end of the part
+                TL t[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    t[e] = s0 + e >= ck.mis && s0 + e < ck.mis + ck.n ? g[s0 + e - ck.mis] : SpElem<TL>::ninf();
+                memcpy(&r[j], t, 16);
+            }
+            reinterpret_cast<uint4*>(ck.buf)[q] = r[j];
+            float v[VEC];
+            SpElem<TL>::unpack(r[j], v);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) mine = fmaxf(mine, v[e]);   // a NaN operand is ignored
+        }
     }
+    float m = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) sm.wsum[warp] = m;
+    if (lane == 0) sm.wmax[warp] = m;
     __syncthreads();
     if (warp == 0) {
-        m = lane < SP_WARPS ? static_cast<float>(sm.wsum[lane]) : -INFINITY;
+        m = lane < SP_WARPS ? sm.wmax[lane] : -INFINITY;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane < static_cast<int>(C)) st_cluster_f32(&sm.cmax[rank], lane, m);
     }
-    cluster_sync_all();
-    m = -INFINITY;
-    for (uint32_t r = 0; r < C; ++r) m = fmaxf(m, sm.cmax[r]);
 
     // ---- the row's parameters
-    const int pr = row / a.per, pj = row % a.per;
-    double T = a.temperature ? static_cast<double>(__ldg(a.temperature + pr)) : 1.0;
-    int k = a.top_k ? __ldg(a.top_k + pr) : 0;
-    double p = a.top_p ? static_cast<double>(__ldg(a.top_p + pr)) : 2.0;
-    double mp = a.min_p ? static_cast<double>(__ldg(a.min_p + pr)) : 0.0;
+    const int seq = row / a.per, pj = row % a.per;
+    double T = a.temperature ? static_cast<double>(__ldg(a.temperature + seq)) : 1.0;
+    SpRow r;
+    r.k = a.top_k ? __ldg(a.top_k + seq) : 0;
+    r.p = a.top_p ? static_cast<double>(__ldg(a.top_p + seq)) : 2.0;
+    double mp = a.min_p ? static_cast<double>(__ldg(a.min_p + seq)) : 0.0;
     if (!(T > 0.0)) {   // greedy
         T = 1.0;
-        k = 1;
-        p = 2.0;
+        r.k = 1;
+        r.p = 2.0;
         mp = 0.0;
     }
-    const bool by_k = k > 0 && k < a.V;
-    const bool by_p = p < 1.0;
-    const double c = 1.4426950408889634 / T;
-    const double md = bits_to_f64(__float_as_uint(m));
+    r.by_k = r.k > 0 && r.k < a.V;
+    r.by_p = r.p < 1.0;
+    r.has_draft = VERIFY && pj < a.per - 1;
+    r.x = -1;
+    r.q = nullptr;
+    r.ua = 0.0;
+    if (r.has_draft) {
+        r.x = __ldg(a.draft + static_cast<size_t>(seq) * (a.per - 1) + pj);
+        if (r.x < 0 || r.x >= a.V) r.x = -1;
+        if (a.q) r.q = a.q + (static_cast<size_t>(seq) * (a.per - 1) + pj) * a.V;
+        r.ua = static_cast<double>(__ldg(a.u + static_cast<size_t>(seq) * a.per + pj));
+    }
+    r.us = static_cast<double>(__ldg(a.u + (VERIFY ? static_cast<size_t>(seq) * a.per + a.per - 1 : static_cast<size_t>(row))));
+    r.us = fmin(r.us, 1.0 - 0x1p-24);
+
+    cluster_sync_all();
+    m = -INFINITY;
+    for (uint32_t i = 0; i < C; ++i) m = fmaxf(m, sm.cmax[i]);
+    const SpScale sc{m, bits_to_f64(__float_as_uint(m)), 1.4426950408889634 / T, sm.tab};
     double dmin = -44.361419555836498 * T;   // 64 ln 2
     if (mp > 0.0) dmin = fmax(dmin, T * log(fmin(mp, 1.0)));
-    SpCut cut;
-    cut.lcut = fmaxf(__double2float_ru(static_cast<double>(m) + dmin), -FLT_MAX);
-    cut.cut = 0;
+    const float lcut = fmaxf(__double2float_ru(static_cast<double>(m) + dmin), -FLT_MAX);
 
-    const bool has_draft = VERIFY && pj < a.per - 1;
     if (m == -INFINITY) {   // nothing can be drawn
         if (rank == 0 && tid == 0) {
             a.token[row] = -1;
@@ -514,153 +1001,132 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(const SampleArgs a) 
         return;
     }
 
-    // ---- top-k and top-p: the composite key of the last token kept
-    if (by_k || by_p) {
-        const uint32_t klo = order_key(cut.lcut) >> KSH, khi = order_key(m) >> KSH;
-        uint32_t key = 0, ties = 0;   // the border key, and how many tokens have it
-        unsigned long long keep = 0;  // how many of those are kept
-        unsigned long long above = 0;
-        uint32_t lo = klo;
-        double S = 0.0;
-        bool cutting = false;
-        if (by_k) {
-            radix_select<TL, false>(sm, ck, rank, C, klo, khi, cut.lcut, md, c, static_cast<double>(k), key, above,
-                                    ties);
-            const unsigned long long want = static_cast<unsigned long long>(k) - min(above, static_cast<unsigned long long>(k));
-            keep = min(want, static_cast<unsigned long long>(ties));
-            lo = key;
-            cutting = true;
+    // ---- few candidates: a list of them, finished by the leader
+    uint32_t n = 0xffffffffu;
+    double S_all = -1.0;
+    float list_lo = lcut;
+    SpBin at{};
+    if (mp > 0.0) n = gather<TL>(sm, ck, rank, C, [&](float l) { return l >= lcut; });
+    if (n > SP_CAP && r.by_k && r.k <= SP_CAP) {
+        list_lo = kth_bound(sm, sc, C, lcut, mine, static_cast<uint32_t>(r.k));
+        n = gather<TL>(sm, ck, rank, C, [&](float l) { return l >= list_lo; });
+    }
+    if (n > SP_CAP && r.by_p && !r.by_k) {
+        at = select_first<TL, true>(sm, ck, sc, rank, C, lcut, -1.0, r.p);
+        S_all = static_cast<double>(at.total) / static_cast<double>(1ull << SP_FIX);
+        if (at.cabove + at.cnt <= SP_CAP) {
+            const SpBins bins = first_bins(sc, lcut);
+            n = gather<TL>(sm, ck, rank, C, [&](float l) { return l >= lcut && bins.of(l) <= at.b; });
         }
-        if (by_p) {
-            // the sum over the top-k tokens: everything above the border key, and its kept ties
-            SpCut all = cut;
-            if (by_k) all.cut = (static_cast<unsigned long long>(key) + 1) << 32;
-            segment_sums<TL>(sm, sm.wsum, ck, rank, C, all, md, c, -1, nullptr, 0.0);
-            S = table_sum(sm.wsum, C, lane);
-            if (by_k) {
-                const float lk = key_value(KSH ? (key << KSH) | ((key >> 15) ? 0u : 0xffffu) : key);
-                S += static_cast<double>(keep) * exp2_64((bits_to_f64(__float_as_uint(lk)) - md) * c, sm.tab);
-            }
-            const double target = fmax(p * S, 1e-9);
-            const uint32_t kkey = key;
-            const unsigned long long kkeep = keep;
-            radix_select<TL, true>(sm, ck, rank, C, lo, khi, cut.lcut, md, c,
-                                   target * static_cast<double>(1ull << SP_FIX), key, above, ties);
-            const float lp = key_value(KSH ? (key << KSH) | ((key >> 15) ? 0u : 0xffffu) : key);
-            const double wp = exp2_64((bits_to_f64(__float_as_uint(lp)) - md) * c, sm.tab);
-            const double need = ceil((target - static_cast<double>(above) / static_cast<double>(1ull << SP_FIX)) / wp);
-            keep = need < 1.0 ? 1 : need >= static_cast<double>(ties) ? ties : static_cast<unsigned long long>(need);
-            if (by_k && key == kkey) keep = min(keep, kkeep);
-            cutting = true;
-        }
-        if (cutting) {
-            cut.cut = static_cast<unsigned long long>(key) << 32;
-            if (keep < ties) {
-                // the index of the keep-th token with the border key, in index order
-                int q0, q1;
-                warp_segment(ck.nvec, warp, q0, q1);
-                const uint4* bv = reinterpret_cast<const uint4*>(ck.buf);
-                uint32_t n = 0;
-                for (int v0 = q0 + lane; v0 < q1; v0 += 32) {
-                    float v[VEC];
-                    SpElem<TL>::unpack(bv[v0], v);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) n += v[e] >= cut.lcut && (order_key(v[e]) >> KSH) == key;
-                }
-                n = __reduce_add_sync(0xffffffffu, n);
-                if (lane == 0) sm.wcnt[warp] = n;
-                __syncthreads();
-                uint32_t tot = 0, before = 0;
-                for (int w = 0; w < SP_WARPS; ++w) {
-                    if (w < warp) before += sm.wcnt[w];
-                    tot += sm.wcnt[w];
-                }
-                if (tid < static_cast<int>(C)) st_cluster_s32(&sm.tie[rank], tid, static_cast<int>(tot));
-                cluster_sync_all();
-                for (uint32_t r = 0; r < rank; ++r) before += sm.tie[r];
-                if (keep > before && keep <= before + n) {
-                    uint32_t left = static_cast<uint32_t>(keep) - before;   // 1-based
-                    for (int v0 = q0; v0 < q1; v0 += 32) {
-                        uint32_t mask = 0;
-                        if (v0 + lane < q1) {
-                            float v[VEC];
-                            SpElem<TL>::unpack(bv[v0 + lane], v);
-#pragma unroll
-                            for (int e = 0; e < VEC; ++e)
-                                mask |= (v[e] >= cut.lcut && (order_key(v[e]) >> KSH) == key ? 1u : 0u) << e;
-                        }
-                        const uint32_t mine = __popc(mask);
-                        const uint32_t in = warp_scan(mine, lane);
-                        if (in >= left && in - mine < left) {
-                            uint32_t skip = left - (in - mine) - 1;
-                            while (skip--) mask &= mask - 1;
-                            const int idx = ck.begin + (v0 + lane) * VEC + (__ffs(mask) - 1) - ck.mis;
-                            for (uint32_t r = 0; r < C; ++r) st_cluster_s32(&sm.cut_idx, r, idx);
-                        }
-                        const uint32_t t = __shfl_sync(0xffffffffu, in, 31);
-                        if (t >= left) break;
-                        left -= t;
-                    }
-                }
-                cluster_sync_all();
-                cut.cut = composite(key, static_cast<int>(sm.cut_idx));
+    }
+    if (n <= SP_CAP) {
+        if (rank == 0) {
+            for (int i = tid; i < static_cast<int>(n); i += SP_THREADS) {
+                uint32_t j = i, c = 0;
+                while (j >= sm.ccnt[c]) j -= sm.ccnt[c++];
+                unsigned long long k;
+                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(sp_mapa(&sm.l.loc[j], c)) : "memory");
+                sm.l.lst[i] = k;
             }
         }
+        cluster_sync_all();   // the other CTAs' lists have been read
+        if (rank == 0)
+            draw_from_list<VERIFY>(sm, static_cast<int>(n), sc, r, S_all, a.token + row, VERIFY ? a.accepted + row : nullptr);
+        if (VERIFY || !a.probs) return;
+        if (rank == 0) {
+            __syncthreads();
+            if (tid < static_cast<int>(C)) {
+                st_cluster_u64(&sm.list_cut, tid, sm.list_cut);
+                st_cluster_f64(&sm.list_sum, tid, sm.list_sum);
+            }
+        }
+        cluster_sync_all();
     }
 
-    // ---- sums, acceptance of the draft, the draw
-    const int seq = row / a.per;
-    int x = -1;
-    double wx = 0.0;
-    const float* q = nullptr;
-    if (has_draft) {
-        x = __ldg(a.draft + static_cast<size_t>(seq) * (a.per - 1) + pj);
-        if (x < 0 || x >= a.V) x = -1;
-        if (a.q) q = a.q + (static_cast<size_t>(seq) * (a.per - 1) + pj) * a.V;
-        if (x >= 0)
-            wx = kept_weight<TL>(SpElem<TL>::load(rowp + x), x, cut, md, c, -1, nullptr, 0.0, sm.tab);
-    }
-    const int skip = has_draft && !q ? x : -1;   // a certain draft leaves the others
-    segment_sums<TL>(sm, sm.wsum, ck, rank, C, cut, md, c, skip, nullptr, 0.0);
-    const double rest = table_sum(sm.wsum, C, lane);
-    const double S = skip >= 0 ? rest + wx : rest;
-    if (has_draft) {
-        const double ua = static_cast<double>(__ldg(a.u + static_cast<size_t>(seq) * a.per + pj));
-        const double qx = q ? (x >= 0 ? static_cast<double>(__ldg(q + x)) : 0.0) : 1.0;
-        if (x >= 0 && ua * qx * S < wx) {
-            if (rank == 0 && tid == 0) {
-                a.token[row] = x;
-                a.accepted[row] = 1;
-            }
-            cluster_sync_all();
-            return;
+    // ---- many: the border of the kept set by selection over the whole row
+    SpCut cut{lcut, INT_MAX};
+    double S = 0.0;
+    if (n <= SP_CAP) {
+        S = sm.list_sum;
+        cut.tau = list_lo;   // the whole list is kept where it has no cut
+        if (sm.list_cut) {
+            cut.tau = composite_value(sm.list_cut);
+            cut.icut = composite_index(sm.list_cut);
         }
-    }
-    const double us = static_cast<double>(VERIFY ? __ldg(a.u + static_cast<size_t>(seq) * a.per + a.per - 1) : __ldg(a.u + row));
-    int tok = -1;
-    if (q) {
-        segment_sums<TL>(sm, sm.rsum, ck, rank, C, cut, md, c, -1, q, S);
-        const bool left = table_sum(sm.rsum, C, lane) > 0.0;
-        if (left) tok = draw_token<TL>(sm, sm.rsum, ck, rank, C, cut, md, c, -1, q, S, us);
-        else tok = draw_token<TL>(sm, sm.wsum, ck, rank, C, cut, md, c, -1, nullptr, 0.0, us);
-    } else if (rest > 0.0) {
-        tok = draw_token<TL>(sm, sm.wsum, ck, rank, C, cut, md, c, skip, nullptr, 0.0, us);
-    } else if (rank == 0 && warp == 0) {
-        tok = x;   // the draft is the only token kept
-    }
-    if (tok >= 0 && lane == 0) {
-        a.token[row] = tok;
-        if (VERIFY) a.accepted[row] = 0;
+    } else {
+        if (r.by_k || r.by_p) {
+            unsigned long long keep = 0;   // how many of the tokens at the border are kept
+            uint32_t key = 0;
+            float lo = lcut;
+            if (r.by_k) {
+                at = select_first<TL, false>(sm, ck, sc, rank, C, lcut, static_cast<double>(r.k), 0.0);
+                key = select_key<TL, false>(sm, ck, sc, rank, C, lcut, static_cast<double>(r.k), at);
+                const unsigned long long want = static_cast<unsigned long long>(r.k) - min(at.above, static_cast<unsigned long long>(r.k));
+                keep = min(want, static_cast<unsigned long long>(at.cnt));
+                lo = key_logit<TL>(key);
+            }
+            if (r.by_p) {
+                const float kth = lo;
+                const unsigned long long kkeep = keep;
+                double target;
+                if (r.by_k) {
+                    // the sum over the top-k tokens: everything above the border, and its kept ties
+                    segment_sums<TL>(sm.wsum, ck, rank, C, SpCut{kth, -1}, sc, -1, nullptr, 0.0);
+                    target = fmax(r.p * (table_sum(sm.wsum, C, lane) + static_cast<double>(keep) * sc.weight(kth)), 1e-9);
+                    at = select_first<TL, true>(sm, ck, sc, rank, C, kth, target * static_cast<double>(1ull << SP_FIX), 0.0);
+                } else {
+                    target = fmax(r.p * S_all, 1e-9);
+                }
+                key = select_key<TL, true>(sm, ck, sc, rank, C, lo, target * static_cast<double>(1ull << SP_FIX), at);
+                lo = key_logit<TL>(key);
+                const double need =
+                    ceil((target - static_cast<double>(at.above) / static_cast<double>(1ull << SP_FIX)) / sc.weight(lo));
+                keep = need < 1.0 ? 1 : need >= static_cast<double>(at.cnt) ? at.cnt : static_cast<unsigned long long>(need);
+                if (r.by_k && lo == kth) keep = min(keep, kkeep);
+            }
+            cut.tau = lo;
+            if (keep < at.cnt) cut.icut = tie_index<TL>(sm, ck, rank, C, lo, static_cast<uint32_t>(keep));
+        }
+        // ---- sums, acceptance of the draft, the draw
+        double wx = 0.0;
+        if (r.x >= 0) wx = kept_weight<TL>(SpElem<TL>::load(rowp + r.x), r.x, cut, sc, -1, nullptr, 0.0);
+        const int skip = r.has_draft && !r.q ? r.x : -1;   // a certain draft leaves the others
+        segment_sums<TL>(sm.wsum, ck, rank, C, cut, sc, skip, nullptr, 0.0);
+        const double rest = table_sum(sm.wsum, C, lane);
+        S = skip >= 0 ? rest + wx : rest;
+        if (r.has_draft) {
+            const double qx = r.q ? (r.x >= 0 ? static_cast<double>(__ldg(r.q + r.x)) : 0.0) : 1.0;
+            if (wx > 0.0 && r.ua * qx * S < wx) {
+                if (rank == 0 && tid == 0) {
+                    a.token[row] = r.x;
+                    a.accepted[row] = 1;
+                }
+                return;
+            }
+        }
+        int tok = -1;
+        if (r.q) {
+            segment_sums<TL>(sm.rsum, ck, rank, C, cut, sc, -1, r.q, S);
+            if (table_sum(sm.rsum, C, lane) > 0.0) tok = draw_token<TL>(sm.rsum, ck, rank, C, cut, sc, -1, r.q, S, r.us);
+            else tok = draw_token<TL>(sm.wsum, ck, rank, C, cut, sc, -1, nullptr, 0.0, r.us);
+        } else if (rest > 0.0) {
+            tok = draw_token<TL>(sm.wsum, ck, rank, C, cut, sc, skip, nullptr, 0.0, r.us);
+        } else if (rank == 0 && warp == 0) {
+            tok = r.x;   // the draft is the only token kept
+        }
+        if (tok >= 0 && lane == 0) {
+            a.token[row] = tok;
+            if (VERIFY) a.accepted[row] = 0;
+        }
     }
     if (!VERIFY && a.probs) {
         float* out = a.probs + static_cast<size_t>(row) * a.V + ck.begin;
         const double inv = 1.0 / S;
         for (int i = tid; i < ck.n; i += SP_THREADS) {
             const float l = static_cast<float>(ck.buf[ck.mis + i]);
-            out[i] = static_cast<float>(kept_weight<TL>(l, ck.begin + i, cut, md, c, -1, nullptr, 0.0, sm.tab) * inv);
+            out[i] = static_cast<float>(kept_weight<TL>(l, ck.begin + i, cut, sc, -1, nullptr, 0.0) * inv);
         }
     }
-    cluster_sync_all();   // no CTA leaves while another may still write to its shared memory
 }
 
 // The verification's last step, one thread per sequence: accepted drafts up to
