@@ -285,13 +285,11 @@ MS_API ms_status spec_sample(const void* logits, ms_dtype logits_dtype, int T, i
  * NULL or as in spec_sample.  u: [B,K+1] fp32 in [0, 1), independent.
  * committed: [B,K+1] int32.  n_committed: [B] int32.  K = 0 (draft may be
  * NULL) is plain sampling.  K <= 8, V <= 262,144, B*(K+1) <= 2^24.
- * Scratch: spec_verify_sample_workspace_size(B,K,V) bytes. */
-MS_API size_t spec_verify_sample_workspace_size(int B, int K, int V);
+ * No scratch. */
 MS_API ms_status spec_verify_sample(const void* logits, ms_dtype logits_dtype, const int32_t* draft,
                                     const float* draft_probs, const float* temperature, const int32_t* top_k,
                                     const float* top_p, const float* min_p, const float* u, int B, int K, int V,
-                                    int32_t* committed, int32_t* n_committed, void* ws, size_t ws_bytes,
-                                    void* stream);
+                                    int32_t* committed, int32_t* n_committed, void* stream);
 
 /* a5 + a6 fused: the vocab head with the verification's argmax in its
  * epilogue, then the prefix match -- the logits are never written.

@@ -32,6 +32,7 @@ constexpr int SP_WARPS = SP_THREADS / 32;
 constexpr int SP_MAXC = 8;              // CTAs of a row's cluster
 constexpr int SP_MAX_CHUNK = 32768;     // elements of a row per CTA (bounds the histogram limbs)
 constexpr int SP_BINS = 1024;
+constexpr int32_t SP_ACCEPTED = -2;
 constexpr int SP_MAX_V = SP_MAXC * SP_MAX_CHUNK;
 constexpr int SP_FIX = 45;              // fixed point of histogram masses: 2^18 weights of 1 fit 63 bits
 constexpr int SP_LIMB = 15;             // 3 limbs; 2^15 elements x 2^15 fit a 32-bit counter
@@ -46,8 +47,7 @@ struct SampleArgs {
     const int32_t* top_k;
     const int32_t* draft;       // verify: [rows / per, per - 1]
     const float* q;             // verify: [rows / per, per - 1, V] or NULL (the draft is certain)
-    int32_t* token;             // [rows]
-    int32_t* accepted;          // verify: [rows]
+    int32_t* token;             // [rows]; verify: SP_ACCEPTED where the row's draft is accepted
     float* probs;               // sample: [rows, V] or NULL
 };
 
@@ -613,8 +613,7 @@ struct SpRow {
 // filters, acceptance of the draft, the draw.  S_all: the row's sum before
 // top-p, or negative where the list is the whole row.
 template <bool VERIFY>
-__device__ void draw_from_list(SampleSmem& sm, int n, const SpScale& sc, const SpRow& r, double S_all, int32_t* token,
-                               int32_t* accepted) {
+__device__ void draw_from_list(SampleSmem& sm, int n, const SpScale& sc, const SpRow& r, double S_all, int32_t* token) {
     const int tid = threadIdx.x;
     const unsigned long long* lst = sm.l.lst;
     unsigned long long* srt = sm.l.loc;
@@ -674,10 +673,7 @@ __device__ void draw_from_list(SampleSmem& sm, int n, const SpScale& sc, const S
         if (!r.q) S = total + wx;
         const double qx = r.q ? (r.x >= 0 ? static_cast<double>(__ldg(r.q + r.x)) : 0.0) : 1.0;
         if (wx > 0.0 && r.ua * qx * S < wx) {
-            if (tid == 0) {
-                *token = r.x;
-                *accepted = 1;
-            }
+            if (tid == 0) *token = SP_ACCEPTED;
             return;
         }
         if (r.q) {
@@ -704,17 +700,11 @@ __device__ void draw_from_list(SampleSmem& sm, int n, const SpScale& sc, const S
         sm.list_sum = S;
     }
     if (!(total > 0.0)) {   // the draft is the only token kept
-        if (tid == 0) {
-            *token = r.x;
-            if (VERIFY) *accepted = 0;
-        }
+        if (tid == 0) *token = r.x;
         return;
     }
     const int e = run_hit(w, start, end, r.us * total);
-    if (e >= 0) {
-        *token = composite_index(lst[tid * per + e]);
-        if (VERIFY) *accepted = 0;
-    }
+    if (e >= 0) *token = composite_index(lst[tid * per + e]);
 }
 
 // ---------------------------------------------------------------- the draw from the whole row
@@ -992,10 +982,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs 
     const float lcut = fmaxf(__double2float_ru(static_cast<double>(m) + dmin), -FLT_MAX);
 
     if (m == -INFINITY) {   // nothing can be drawn
-        if (rank == 0 && tid == 0) {
-            a.token[row] = -1;
-            if (VERIFY) a.accepted[row] = 0;
-        }
+        if (rank == 0 && tid == 0) a.token[row] = -1;
         if (!VERIFY && a.probs)
             for (int i = tid; i < ck.n; i += SP_THREADS) a.probs[static_cast<size_t>(row) * a.V + ck.begin + i] = 0.f;
         return;
@@ -1031,7 +1018,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs 
         }
         cluster_sync_all();   // the other CTAs' lists have been read
         if (rank == 0)
-            draw_from_list<VERIFY>(sm, static_cast<int>(n), sc, r, S_all, a.token + row, VERIFY ? a.accepted + row : nullptr);
+            draw_from_list<VERIFY>(sm, static_cast<int>(n), sc, r, S_all, a.token + row);
         if (VERIFY || !a.probs) return;
         if (rank == 0) {
             __syncthreads();
@@ -1097,10 +1084,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs 
         if (r.has_draft) {
             const double qx = r.q ? (r.x >= 0 ? static_cast<double>(__ldg(r.q + r.x)) : 0.0) : 1.0;
             if (wx > 0.0 && r.ua * qx * S < wx) {
-                if (rank == 0 && tid == 0) {
-                    a.token[row] = r.x;
-                    a.accepted[row] = 1;
-                }
+                if (rank == 0 && tid == 0) a.token[row] = SP_ACCEPTED;
                 return;
             }
         }
@@ -1114,10 +1098,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs 
         } else if (rank == 0 && warp == 0) {
             tok = r.x;   // the draft is the only token kept
         }
-        if (tok >= 0 && lane == 0) {
-            a.token[row] = tok;
-            if (VERIFY) a.accepted[row] = 0;
-        }
+        if (tok >= 0 && lane == 0) a.token[row] = tok;
     }
     if (!VERIFY && a.probs) {
         float* out = a.probs + static_cast<size_t>(row) * a.V + ck.begin;
@@ -1129,21 +1110,24 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs 
     }
 }
 
-// The verification's last step, one thread per sequence: accepted drafts up to
-// the first rejection, then the token drawn at that position.
-__global__ void __launch_bounds__(128) sample_commit_kernel(const int32_t* __restrict__ token,
-                                                            const int32_t* __restrict__ accepted, int B, int K,
+// The verification's last step, one thread per sequence: the rows' results in
+// committed become the accepted drafts up to the first rejection, the token
+// drawn there, and padding.
+__global__ void __launch_bounds__(128) sample_commit_kernel(const int32_t* __restrict__ draft, int B, int K,
                                                             int32_t* __restrict__ committed,
                                                             int32_t* __restrict__ n_committed) {
     grid_dep_wait();
     grid_dep_launch();
     const int b = blockIdx.x * blockDim.x + threadIdx.x;
     if (b >= B) return;
-    const size_t base = static_cast<size_t>(b) * (K + 1);
+    int32_t* row = committed + static_cast<size_t>(b) * (K + 1);
     int n = 0;
-    while (n < K && accepted[base + n]) ++n;
-    for (int j = 0; j <= K; ++j) committed[base + j] = j <= n ? token[base + j] : -1;
-    n_committed[b] = n + (token[base + n] >= 0 ? 1 : 0);
+    while (n < K && row[n] == SP_ACCEPTED) {
+        row[n] = draft[static_cast<size_t>(b) * K + n];
+        ++n;
+    }
+    for (int j = n + 1; j <= K; ++j) row[j] = -1;
+    n_committed[b] = n + (row[n] >= 0 ? 1 : 0);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1168,10 +1152,6 @@ static ms_status sample_launch(SampleArgs a, ms_dtype dt, bool verify, cudaStrea
     if (dt == MS_BF16)
         return verify ? sample_launch_t<__nv_bfloat16, true>(a, s) : sample_launch_t<__nv_bfloat16, false>(a, s);
     return verify ? sample_launch_t<float, true>(a, s) : sample_launch_t<float, false>(a, s);
-}
-
-static size_t verify_sample_ws_bytes(int B, int K) {
-    return 2 * align_up(static_cast<size_t>(B) * (K + 1) * sizeof(int32_t), 256);
 }
 
 // Rows and vocabulary that one launch can take.
@@ -1202,23 +1182,15 @@ extern "C" ms_status spec_sample(const void* logits, ms_dtype logits_dtype, int 
     return ms::sample_launch(a, logits_dtype, false, static_cast<cudaStream_t>(stream));
 }
 
-extern "C" size_t spec_verify_sample_workspace_size(int B, int K, int V) {
-    if (B <= 0 || K < 0 || V <= 0) return 0;
-    return ms::verify_sample_ws_bytes(B, K);
-}
-
 extern "C" ms_status spec_verify_sample(const void* logits, ms_dtype logits_dtype, const int32_t* draft,
                                         const float* draft_probs, const float* temperature, const int32_t* top_k,
                                         const float* top_p, const float* min_p, const float* u, int B, int K, int V,
-                                        int32_t* committed, int32_t* n_committed, void* ws, size_t ws_bytes,
-                                        void* stream) {
+                                        int32_t* committed, int32_t* n_committed, void* stream) {
     if (!logits || (K > 0 && !draft) || !u || !committed || !n_committed) return MS_ERR_INVALID_ARG;
     if (B <= 0 || V <= 0 || K < 0) return MS_ERR_INVALID_ARG;
     if (logits_dtype != MS_F32 && logits_dtype != MS_BF16) return MS_ERR_INVALID_ARG;
     if (!ms::element_aligned(logits, logits_dtype)) return MS_ERR_INVALID_ARG;
     if (K > 8 || !ms::sample_size_ok(static_cast<long>(B) * (K + 1), V)) return MS_ERR_UNSUPPORTED;
-    if (!ws || ws_bytes < ms::verify_sample_ws_bytes(B, K)) return MS_ERR_WORKSPACE;
-    if (!ms::aligned16(ws)) return MS_ERR_INVALID_ARG;
     ms::SampleArgs a{};
     a.logits = logits;
     a.V = V;
@@ -1231,12 +1203,10 @@ extern "C" ms_status spec_verify_sample(const void* logits, ms_dtype logits_dtyp
     a.u = u;
     a.draft = draft;
     a.q = K > 0 ? draft_probs : nullptr;
-    a.token = static_cast<int32_t*>(ws);
-    a.accepted = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + ms::verify_sample_ws_bytes(B, K) / 2);
+    a.token = committed;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const ms_status st = ms::sample_launch(a, logits_dtype, true, s);
     if (st != MS_OK) return st;
     return ms::launch(ms::K_SAMPLE_COMMIT, ms::sample_commit_kernel, dim3((B + 127) / 128), dim3(128), 0, s,
-                      static_cast<const int32_t*>(a.token), static_cast<const int32_t*>(a.accepted), B, K, committed,
-                      n_committed);
+                      draft, B, K, committed, n_committed);
 }

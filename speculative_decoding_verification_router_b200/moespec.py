@@ -50,8 +50,7 @@ def _load():
         "moe_combine": (I, [P, I, P, P, P, P, I, I, I, P, P, P]),
         "moe_route_grouped": (I, [P, I, P, I, I, I, I, I, I, I, I, F, P, P, P]),
         "spec_sample": (I, [P, I, I, I, P, P, P, P, P, P, P, P]),
-        "spec_verify_sample_workspace_size": (Z, [I, I, I]),
-        "spec_verify_sample": (I, [P, I, P, P, P, P, P, P, P, I, I, I, P, P, P, Z, P]),
+        "spec_verify_sample": (I, [P, I, P, P, P, P, P, P, P, I, I, I, P, P, P]),
         "lm_head_workspace_size": (Z, [I, I, I]),
         "lm_head_logits": (I, [P, P, I, I, I, P, P, Z, P]),
         "spec_verify_workspace_size": (Z, [I, I, I]),
@@ -157,24 +156,21 @@ def _filters(n: int, dev, temperature, top_k, top_p, min_p):
         _vec(min_p, torch.float32, (n,), "min_p", dev)
 
 
-class _Here:
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-_here = _Here()
-
-
-def _on(dev):
-    """Makes a tensor's device current for the call (a no-op where it already is)."""
-    return _here if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
-def _raw_stream(dev, stream):
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+def _launch(fn, where: str, dev, stream, *args):
+    """Calls fn(*args, stream) with dev current, on its current stream unless one is given."""
+    s = _current_stream(dev.index) if stream is None else stream.cuda_stream
+    if dev.index == _current_device():
+        code = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, s)
+    if code != 0:
+        raise MoeSpecError(code, where)
 
 
 class Workspace:
@@ -293,17 +289,15 @@ def route_grouped(logits: torch.Tensor, k: int, score: str = "softmax", bias: Op
     if bias is not None:
         _vec(bias, torch.float32, (E,), "bias", dev)
     if out is None:
-        idx = torch.empty((T, k), dtype=torch.int32, device=dev)
-        w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+        w = torch.empty(T, k, dtype=torch.float32, device=dev)
     else:
         idx, w = out
         _vec(idx, torch.int32, (T, k), "out[0]", dev)
         _vec(w, torch.float32, (T, k), "out[1]", dev)
-    with _on(dev):
-        _check(_lib.moe_route_grouped(logits.data_ptr(), _LOGITS[logits.dtype], _a(bias), T, E, _SCORES[score],
-                                      n_groups, n_groups if topk_groups is None else topk_groups, group_top, k,
-                                      int(renormalize), scale, idx.data_ptr(), w.data_ptr(), _raw_stream(dev, stream)),
-               "moe_route_grouped")
+    _launch(_lib.moe_route_grouped, "moe_route_grouped", dev, stream, logits.data_ptr(), _LOGITS[logits.dtype],
+            _a(bias), T, E, _SCORES[score], n_groups, n_groups if topk_groups is None else topk_groups, group_top, k,
+            1 if renormalize else 0, scale, idx.data_ptr(), w.data_ptr())
     return idx, w
 
 
@@ -406,16 +400,13 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
         _vec(token, torch.int32, (T,), "out token", dev)
         if probs is not None:
             _vec(probs, torch.float32, (T, V), "out probs", dev)
-    with _on(dev):
-        _check(_lib.spec_sample(logits.data_ptr(), _LOGITS[logits.dtype], T, V, _a(temperature), _a(top_k), _a(top_p),
-                                _a(min_p), u.data_ptr(), token.data_ptr(), _a(probs), _raw_stream(dev, stream)),
-               "spec_sample")
+    _launch(_lib.spec_sample, "spec_sample", dev, stream, logits.data_ptr(), _LOGITS[logits.dtype], T, V,
+            _a(temperature), _a(top_k), _a(top_p), _a(min_p), u.data_ptr(), token.data_ptr(), _a(probs))
     return (token, probs) if return_probs else token
 
 
 def verify_sample(logits: torch.Tensor, draft: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None,
-                  top_p=None, min_p=None, draft_probs: Optional[torch.Tensor] = None,
-                  ws: Optional[Workspace] = None, out=None, stream=None):
+                  top_p=None, min_p=None, draft_probs: Optional[torch.Tensor] = None, out=None, stream=None):
     """Speculative verification of sampled decoding: logits [B, K+1, V] (fp32 or bf16),
     draft [B, K] int32, u [B, K+1] in [0, 1), per-sequence temperature, top_k, top_p,
     min_p ([B] tensors or None), draft_probs [B, K, V] fp32 (None: the drafts were
@@ -429,18 +420,15 @@ def verify_sample(logits: torch.Tensor, draft: torch.Tensor, u: torch.Tensor, te
     if draft_probs is not None:
         _vec(draft_probs, torch.float32, (B, K, V), "draft_probs", dev)
     if out is None:
-        cm = torch.empty((B, K1), dtype=torch.int32, device=dev)
+        cm = torch.empty(B, K1, dtype=torch.int32, device=dev)
         n = torch.empty(B, dtype=torch.int32, device=dev)
     else:
         cm, n = out
         _vec(cm, torch.int32, (B, K1), "out[0]", dev)
         _vec(n, torch.int32, (B,), "out[1]", dev)
-    w = _ws(ws, _lib.spec_verify_sample_workspace_size(B, K, V), dev)
-    with _on(dev):
-        _check(_lib.spec_verify_sample(logits.data_ptr(), _LOGITS[logits.dtype], draft.data_ptr() if K else None,
-                                       _a(draft_probs), _a(temperature), _a(top_k), _a(top_p), _a(min_p),
-                                       u.data_ptr(), B, K, V, cm.data_ptr(), n.data_ptr(), w.ptr, w.nbytes,
-                                       _raw_stream(dev, stream)), "spec_verify_sample")
+    _launch(_lib.spec_verify_sample, "spec_verify_sample", dev, stream, logits.data_ptr(), _LOGITS[logits.dtype],
+            draft.data_ptr() if K else None, _a(draft_probs), _a(temperature), _a(top_k), _a(top_p), _a(min_p),
+            u.data_ptr(), B, K, V, cm.data_ptr(), n.data_ptr())
     return cm, n
 
 

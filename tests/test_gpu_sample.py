@@ -287,17 +287,15 @@ def test_committed_tokens_follow_the_sampled_distribution(ms, certain):
     assert 1 < float(n.float().mean()) < K + 1
 
 
-def test_verify_sample_captured_with_its_own_workspace(ms):
+def test_verify_sample_captured(ms):
     B, K, V = 4, 3, 30011
     z, u = torch.empty(B, K + 1, V, device="cuda"), torch.empty(B, K + 1, device="cuda")
     d = torch.zeros(B, K, dtype=torch.int32, device="cuda")
     k = torch.full((B,), 20, dtype=torch.int32, device="cuda")
-    ws = ms.Workspace(ms.lib().spec_verify_sample_workspace_size(B, K, V))
-    ws.view().fill_(0xff)
     out = (torch.empty(B, K + 1, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda"))
     z.normal_()
     u.uniform_()
-    graph = ms.CapturedStep(lambda: ms.verify_sample(z, d, u, top_k=k, ws=ws, out=out))
+    graph = ms.CapturedStep(lambda: ms.verify_sample(z, d, u, top_k=k, out=out))
     for seed in range(3):
         g = torch.Generator(device="cuda").manual_seed(seed)
         z.normal_(generator=g).mul_(2)

@@ -31,18 +31,12 @@ def test_sample_refusals(ms, change, code):
 @pytest.mark.parametrize("change,code", [
     (dict(logits=None), -1), (dict(draft=None), -1), (dict(u=None), -1), (dict(cm=None), -1), (dict(n=None), -1),
     (dict(B=0), -1), (dict(K=-1), -1), (dict(V=0), -1), (dict(dt=5), -1), (dict(K=9), -2), (dict(V=262145), -2),
-    (dict(ws=None), -3), (dict(wsb=8), -3), (dict(ws=P(4100)), -1), (dict(logits=P(4098)), -1)])
+    (dict(logits=P(4098)), -1)])
 def test_verify_sample_refusals(ms, change, code):
-    a = dict(logits=FAKE, dt=0, draft=FAKE, u=FAKE, B=2, K=3, V=1000, cm=FAKE, n=FAKE, ws=FAKE, wsb=1 << 20)
+    a = dict(logits=FAKE, dt=0, draft=FAKE, u=FAKE, B=2, K=3, V=1000, cm=FAKE, n=FAKE)
     a.update(change)
     assert ms.lib().spec_verify_sample(a["logits"], a["dt"], a["draft"], None, None, None, None, None, a["u"], a["B"],
-                                       a["K"], a["V"], a["cm"], a["n"], a["ws"], a["wsb"], None) == code
-
-
-def test_verify_sample_workspace_size(ms):
-    size = ms.lib().spec_verify_sample_workspace_size
-    assert size(32, 3, 129280) >= 2 * 4 * 32 * 4
-    assert size(0, 3, 100) == 0 and size(2, -1, 100) == 0 and size(2, 3, 0) == 0
+                                       a["K"], a["V"], a["cm"], a["n"], None) == code
 
 
 @pytest.mark.parametrize("change,code", [
