@@ -37,7 +37,7 @@ constexpr int SP_MAX_V = SP_MAXC * SP_MAX_CHUNK;
 constexpr int SP_FIX = 45;              // fixed point of histogram masses: 2^18 weights of 1 fit 63 bits
 constexpr int SP_LIMB = 15;             // 3 limbs; 2^15 elements x 2^15 fit a 32-bit counter
 constexpr int SP_CAP = 2048;            // candidates of a row that the leader finishes from a list
-static_assert(SP_BINS == 2 * SP_THREADS, "the bin scan gives every thread two bins");
+constexpr int SP_BPT = SP_BINS / SP_THREADS;   // bins per thread of a bin scan
 
 struct SampleArgs {
     const void* logits;         // [rows, V]
@@ -71,12 +71,12 @@ __device__ __forceinline__ void red_cluster_u64(const void* local, uint32_t rank
     asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(sp_mapa(local, rank)), "l"(v) : "memory");
 }
 
-// The bits of a float as a double.  Zero and subnormals become about 2^-127,
-// which no difference of logits can see; infinities become +-2^128 (masked
-// tokens are sorted out by comparisons on the float itself).
-__device__ __forceinline__ double bits_to_f64(uint32_t u) {
-    const uint32_t hi = (u & 0x80000000u) | (((u & 0x7fffffffu) >> 3) + 0x38000000u);
-    return __hiloint2double(static_cast<int>(hi), static_cast<int>(u << 29));
+// A float times 2^-896 as a double: its bits shifted into place, without the
+// exponent's bias.  Infinities become +-2^-768 (masked tokens are sorted out by
+// comparisons on the float itself).
+__device__ __forceinline__ double scaled_f64(float l) {
+    const int u = __float_as_int(l);
+    return __hiloint2double((u >> 3) & static_cast<int>(0x8fffffffu), u << 29);
 }
 
 // Floats in ascending order as unsigned integers (-0 equal to +0).
@@ -88,22 +88,38 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// 2^t for -65 < t <= 0, relative error about 2e-13: 2^(k/16) from a table of
-// 16 doubles (one per pair of shared-memory banks: no conflicts whatever the
-// lanes ask for) times the Taylor polynomial of degree 5 of 2^r, |r| <= 1/32.
-__device__ __forceinline__ double exp2_64(double t, const double* tab) {
-    constexpr double kMagic = 422212465065984.0;   // 1.5 * 2^48: adding it rounds t to multiples of 1/16
-    const double z = t + kMagic;
-    const int k = __double2loint(z);
-    const double r = t - (z - kMagic);
-    double p = fma(r, 1.3333558146428443e-3, 9.6181291076284772e-3);   // ln2^5/5!, ln2^4/4!
-    p = fma(p, r, 5.5504108664821580e-2);                              // ln2^3/3!
-    p = fma(p, r, 2.4022650695910071e-1);                              // ln2^2/2!
-    p = fma(p, r, 6.9314718055994531e-1);                              // ln2
-    const double base = tab[k & 15];
-    const double v = fma(base, p * r, base);
-    return __hiloint2double(__double2hiint(v) + ((k >> 4) << 20), __double2loint(v));
-}
+// A row's weights w(l) = 2^((l - max) c), c = log2(e) / T, for -65 < (l - max) c
+// <= 0, to about 2e-13 relative and exactly 1 at the maximum: t = k/16 + r,
+// 2^(k/16) from a table of 16 doubles (one per pair of shared-memory banks: no
+// conflicts whatever the lanes ask for) times the Taylor polynomial of degree 5
+// of 2^r, |r| <= 1/32.  11 fp64 instructions with the sum, 20 in all.
+// The coefficients come from constant memory as operands of the fp64
+// instructions; as literals each took two moves per use.
+__constant__ double kPow2[6] = {1.5 * 281474976710656.0, 6.9314718055994531e-1, 2.4022650695910071e-1,
+                                5.5504108664821580e-2,   9.6181291076284772e-3, 1.3333558146428443e-3};
+struct SpScale {
+    float m;          // max l
+    double md, cs;    // max l times 2^-896, c times 2^896
+    double c;
+    const double* tab;
+    __device__ __forceinline__ double weight(float l) const { return weight(scaled_f64(l), tab); }
+    // the same from a scaled logit; a table times x gives weights times x
+    __device__ __forceinline__ double weight(double l, const double* tab) const {
+        const double kMagic = kPow2[0];   // 1.5 * 2^48: adding it rounds t to multiples of 1/16
+        const double d = l - md;
+        const double z = fma(d, cs, kMagic);
+        const int k = __double2loint(z);
+        const double r = fma(d, cs, kMagic - z);
+        double p = fma(r, kPow2[5], kPow2[4]);   // ln2^5/5!, ln2^4/4!
+        p = fma(p, r, kPow2[3]);                 // ln2^3/3!
+        p = fma(p, r, kPow2[2]);                 // ln2^2/2!
+        p = fma(p, r, kPow2[1]);                 // ln2
+        // the table's high words lack j << 16, which k << 16 brings besides the exponent
+        const double b = tab[k & 15];
+        const double base = __hiloint2double(__double2hiint(b) + (k << 16), __double2loint(b));
+        return fma(base * r, p, base);
+    }
+};
 
 __device__ __forceinline__ double warp_sum_f64(double v) {
 #pragma unroll
@@ -120,23 +136,56 @@ __device__ __forceinline__ T warp_scan(T v, int lane) {   // inclusive
     return v;
 }
 
+// The elements of a 16-byte vector.
 template <typename TL>
 struct SpElem;
 template <>
 struct SpElem<float> {
     static constexpr int VEC = 4;
     static constexpr int KSH = 0;
+    using Bound = float;   // a threshold as the comparisons below want it
+    static __device__ __forceinline__ Bound bound(float t) { return t; }
     static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[4]) {
         v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y);
         v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
     }
-    static __device__ __forceinline__ float load(const float* p) { return __ldg(p); }
+    static __device__ __forceinline__ double scaled(const uint4& r, int e) {
+        return scaled_f64(__uint_as_float(e == 0 ? r.x : e == 1 ? r.y : e == 2 ? r.z : r.w));
+    }
+    // NaN elements are ignored in any_ge and fail all_ge
+    static __device__ __forceinline__ bool any_ge(const uint4& r, Bound t) {
+        return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
+                     fmaxf(__uint_as_float(r.z), __uint_as_float(r.w))) >= t;
+    }
+    static __device__ __forceinline__ bool all_ge(const uint4& r, Bound t) {
+        return __uint_as_float(r.x) >= t && __uint_as_float(r.y) >= t && __uint_as_float(r.z) >= t &&
+               __uint_as_float(r.w) >= t;
+    }
+    struct Max {
+        float m = -INFINITY;
+        __device__ __forceinline__ void add(const uint4& r) {
+            m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(r.x), __uint_as_float(r.y))),
+                      fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+        }
+        __device__ __forceinline__ float get() const { return m; }
+    };
     static __device__ __forceinline__ float ninf() { return -INFINITY; }
 };
 template <>
 struct SpElem<__nv_bfloat16> {
     static constexpr int VEC = 8;
     static constexpr int KSH = 16;   // the low half of a widened bf16 carries nothing
+    using Bound = __nv_bfloat162;
+    // l >= t for bf16 l holds exactly where l >= t rounded up to bf16
+    static __device__ __forceinline__ Bound bound(float t) {
+        const __nv_bfloat16 b = __float2bfloat16_ru(t);
+        return __halves2bfloat162(b, b);
+    }
+    static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t q) {
+        __nv_bfloat162 x;
+        memcpy(&x, &q, 4);
+        return x;
+    }
     static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[8]) {
         const uint32_t q[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -145,20 +194,38 @@ struct SpElem<__nv_bfloat16> {
             v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
         }
     }
-    static __device__ __forceinline__ float load(const __nv_bfloat16* p) {
-        return bf16_to_f32(__ldg(reinterpret_cast<const uint16_t*>(p)));
+    static __device__ __forceinline__ double scaled(const uint4& r, int e) {
+        const uint32_t q = e < 2 ? r.x : e < 4 ? r.y : e < 6 ? r.z : r.w;
+        const int u = static_cast<int>(e & 1 ? q : q << 16);
+        return __hiloint2double((u >> 3) & static_cast<int>(0x8fffe000u), 0);
     }
+    static __device__ __forceinline__ bool any_ge(const uint4& r, Bound t) {
+        const __nv_bfloat162 m = __hmax2(__hmax2(pair(r.x), pair(r.y)), __hmax2(pair(r.z), pair(r.w)));
+        return __hge(__low2bfloat16(m), __low2bfloat16(t)) || __hge(__high2bfloat16(m), __low2bfloat16(t));
+    }
+    static __device__ __forceinline__ bool all_ge(const uint4& r, Bound t) {
+        return __hbge2(__hmin2_nan(__hmin2_nan(pair(r.x), pair(r.y)), __hmin2_nan(pair(r.z), pair(r.w))), t);
+    }
+    struct Max {
+        __nv_bfloat162 m = __halves2bfloat162(__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80));
+        __device__ __forceinline__ void add(const uint4& r) {
+            m = __hmax2(m, __hmax2(__hmax2(pair(r.x), pair(r.y)), __hmax2(pair(r.z), pair(r.w))));
+        }
+        __device__ __forceinline__ float get() const {
+            return fmaxf(__bfloat162float(__low2bfloat16(m)), __bfloat162float(__high2bfloat16(m)));
+        }
+    };
     static __device__ __forceinline__ __nv_bfloat16 ninf() { return __ushort_as_bfloat16(0xff80); }
 };
 
 // Row masses by logit interval, and the candidate lists; never in use together.
 struct SampleSmem {
-    double tab[16];
+    double tab[16], ptab[16];                 // 2^(j/16), and the same over the row's sum
     double wsum[SP_MAXC * SP_WARPS];          // every warp's sum, of every CTA of the cluster
     double rsum[SP_MAXC * SP_WARPS];          // the same for the residual
-    double dscan[SP_WARPS];
+    double dscan[SP_WARPS], dscan2[SP_WARPS];
     unsigned long long scan[SP_WARPS];
-    unsigned long long sel_above, sel_total;  // broadcast results of a selection round
+    unsigned long long sel_above;             // broadcast results of a selection round
     unsigned long long list_cut;              // broadcast results of a list: composite key of the last token kept,
     double list_sum;                          // and the sum of the kept weights
     double wx;
@@ -178,7 +245,9 @@ struct SampleSmem {
     uint32_t tie[SP_MAXC];
     float wmax[SP_WARPS];
     uint32_t wcnt[SP_WARPS];
-    uint32_t sel_bin, sel_cnt, sel_cabove;
+    uint32_t sel_bin, sel_cnt;
+    uint32_t nb0, nb1, nn;                    // leader: the top-p border's intervals, and the tokens down to them
+    uint32_t nuc[3];                          // the same, broadcast
     uint32_t cut_idx;                         // broadcast: index of the last tied token kept
     int last;
     uint32_t keep;
@@ -194,23 +263,19 @@ struct SpChunk {
     __device__ __forceinline__ void load(int vec, float (&v)[SpElem<TL>::VEC]) const {
         SpElem<TL>::unpack(reinterpret_cast<const uint4*>(buf)[vec], v);
     }
-};
-
-// The row's weights: w(l) = 2^((l - max) c), c = log2(e) / T.
-struct SpScale {
-    float m;        // max l
-    double md, c;
-    const double* tab;
-    __device__ __forceinline__ double weight(float l) const {
-        return exp2_64((bits_to_f64(__float_as_uint(l)) - md) * c, tab);
+    // a vector, of -inf at and behind `end`
+    __device__ __forceinline__ uint4 raw_to(int vec, int end) const {
+        constexpr uint32_t kNone = sizeof(TL) == 2 ? 0xff80ff80u : 0xff800000u;
+        return vec < end ? reinterpret_cast<const uint4*>(buf)[vec] : make_uint4(kNone, kNone, kNone, kNone);
     }
-};
-
-// A kept set: logits above tau, and those equal to it up to index icut.
-struct SpCut {
-    float tau;
-    int icut;
-    __device__ __forceinline__ bool keeps(float l, int idx) const { return l > tau || (l == tau && idx <= icut); }
+    __device__ __forceinline__ void load_to(int vec, int end, float (&v)[SpElem<TL>::VEC]) const {
+        SpElem<TL>::unpack(raw_to(vec, end), v);
+    }
+    // leaves element idx of the row out of every later pass
+    __device__ __forceinline__ void mask(int idx) const {
+        const int i = idx - begin;
+        if (i >= 0 && i < n) buf[mis + i] = SpElem<TL>::ninf();
+    }
 };
 
 // Tokens in descending order: (logit, lower index first) as one integer.
@@ -230,86 +295,84 @@ __device__ __forceinline__ void warp_segment(int nvec, int warp, int& q0, int& q
     q1 = min(nvec, q0 + per);
 }
 
+// Sum of the table, the same in every thread of the cluster.
+__device__ double table_sum(const double* sums, uint32_t C, int lane) {
+    double s = 0.0;
+    for (int i = lane; i < static_cast<int>(C) * SP_WARPS; i += 32) s += sums[i];
+    return warp_sum_f64(s);
+}
+
 // ---------------------------------------------------------------- selection
 // Logit intervals of equal width below the maximum; the last one takes the rest.
 struct SpBins {
     float m, s;
+    // a bound below every logit of intervals 0..b that is at least lo, by more than the rounding of of()
+    __device__ __forceinline__ float lower(uint32_t b, float lo) const {
+        if (b >= SP_BINS - 1 || !(s > 0.f)) return lo;
+        return fmaxf(lo, m - (static_cast<float>(b) + 0.5f) / s * (1.f + 1e-6f) - fabsf(m) * 3e-7f);
+    }
     __device__ __forceinline__ uint32_t of(float l) const {
-        return min(static_cast<uint32_t>((m - l) * s), static_cast<uint32_t>(SP_BINS - 1));   // NaN (inf - inf): 0
+        // adding 2^23 leaves the rounded product in the low bits; infinities and NaN (inf - inf) end in the last one
+        return min(__float_as_uint(fmaf(m - l, s, 8388608.f)) - 0x4b000000u, static_cast<uint32_t>(SP_BINS - 1));
     }
 };
 
 struct SpBin {
-    uint32_t b, cnt, cabove;            // the interval, its tokens, the tokens above it
-    unsigned long long above, total;    // masses (or counts) above it, and of the row
+    uint32_t b, cnt;            // the interval, and its tokens
+    unsigned long long above;   // mass (or count) above it
 };
 
 // The leader's part of a selection round: merges the tables, scans them from
 // the top and broadcasts the first interval where `above` + the running total
-// reaches the target (`frac` of the round's total where target < 0).
+// reaches the target.
 template <bool MASS>
-__device__ void select_bin(SampleSmem& sm, uint32_t C, unsigned long long above, uint32_t cabove, double target,
-                           double frac) {
+__device__ void select_bin(SampleSmem& sm, uint32_t C, unsigned long long above, double target) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned long long v[2];
-    uint32_t n[2];
+    unsigned long long v[SP_BPT], own = 0;
+    uint32_t n[SP_BPT];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int i = 2 * tid + j;
+    for (int j = 0; j < SP_BPT; ++j) {
+        const int i = SP_BPT * tid + j;
         n[j] = sm.cnt[i];
         v[j] = n[j];
         if (MASS)
             v[j] = sm.h.mass[i] + sm.h.limb[0][i] + (static_cast<unsigned long long>(sm.h.limb[1][i]) << SP_LIMB) +
                    (static_cast<unsigned long long>(sm.h.limb[2][i]) << (2 * SP_LIMB));
         if (n[j]) atomicMax(&sm.last, i);
+        own += v[j];
     }
-    const unsigned long long own = v[0] + v[1];
     const unsigned long long inc = warp_scan(own, lane);
-    const uint32_t cown = n[0] + n[1];
-    const uint32_t cinc = warp_scan(cown, lane);
-    if (lane == 31) {
-        sm.scan[warp] = inc;
-        sm.wcnt[warp] = cinc;
-    }
+    if (lane == 31) sm.scan[warp] = inc;
     __syncthreads();
     unsigned long long ex = above + inc - own, tot = above;
-    uint32_t cex = cabove + cinc - cown;
     for (int w = 0; w < SP_WARPS; ++w) {
-        if (w < warp) {
-            ex += sm.scan[w];
-            cex += sm.wcnt[w];
-        }
+        if (w < warp) ex += sm.scan[w];
         tot += sm.scan[w];
     }
-    if (target < 0.0) target = fmax(frac * static_cast<double>(tot), 0.5);
     // the last occupied interval where rounding left the target above the total
     const bool never = static_cast<double>(tot) < target;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const bool hit = never ? 2 * tid + j == sm.last
+    for (int j = 0; j < SP_BPT; ++j) {
+        const bool hit = never ? SP_BPT * tid + j == sm.last
                                : n[j] && static_cast<double>(ex) < target && static_cast<double>(ex + v[j]) >= target;
         if (hit)
             for (uint32_t r = 0; r < C; ++r) {
-                st_cluster_s32(&sm.sel_bin, r, 2 * tid + j);
+                st_cluster_s32(&sm.sel_bin, r, SP_BPT * tid + j);
                 st_cluster_s32(&sm.sel_cnt, r, static_cast<int>(n[j]));
-                st_cluster_s32(&sm.sel_cabove, r, static_cast<int>(cex));
                 st_cluster_u64(&sm.sel_above, r, ex);
-                st_cluster_u64(&sm.sel_total, r, tot);
             }
         ex += v[j];
-        cex += n[j];
     }
 }
 
 // One selection round over the cluster's part of the row: a histogram of the
 // elements that bin_of() accepts (counts always, fixed-point masses when MASS),
-// merged and scanned by the leader.  Elements of the last interval are summed
-// in registers when LAST: it takes the bulk of a peaked row.
-template <typename TL, bool MASS, bool LAST, typename F>
+// merged and scanned by the leader.
+template <typename TL, bool MASS, typename F>
 __device__ SpBin select_round(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
-                              unsigned long long above, uint32_t cabove, double target, double frac, F bin_of) {
+                              unsigned long long above, double target, F bin_of) {
     constexpr int VEC = SpElem<TL>::VEC;
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     for (int i = tid; i < SP_BINS; i += SP_THREADS) {
         sm.cnt[i] = 0;
         if (MASS) {
@@ -319,8 +382,6 @@ __device__ SpBin select_round(SampleSmem& sm, const SpChunk<TL>& ck, const SpSca
     }
     if (tid == 0) sm.last = 0;
     cluster_sync_all();   // the leader's tables are clear before anyone adds to them
-    uint32_t rest_n = 0;
-    unsigned long long rest = 0;
     for (int q = tid; q < ck.nvec; q += SP_THREADS) {
         float v[VEC];
         ck.load(q, v);
@@ -328,37 +389,14 @@ __device__ SpBin select_round(SampleSmem& sm, const SpChunk<TL>& ck, const SpSca
         for (int e = 0; e < VEC; ++e) {
             uint32_t bin;
             if (!bin_of(v[e], bin)) continue;
-            unsigned long long W = 0;
+            atomicAdd(&sm.cnt[bin], 1u);
             if (MASS) {
                 // adding 2^7 leaves the weight as an integer of 2^-45 in the low mantissa bits
                 const double z = sc.weight(v[e]) + 128.0;
-                W = static_cast<unsigned long long>(__double_as_longlong(z)) & 0xfffffffffffffull;
-            }
-            if (LAST && bin == SP_BINS - 1) {
-                ++rest_n;
-                rest += W;
-                continue;
-            }
-            atomicAdd(&sm.cnt[bin], 1u);
-            if (MASS) {
+                const unsigned long long W = static_cast<unsigned long long>(__double_as_longlong(z)) & 0xfffffffffffffull;
                 atomicAdd(&sm.h.limb[0][bin], static_cast<uint32_t>(W) & ((1u << SP_LIMB) - 1));
                 atomicAdd(&sm.h.limb[1][bin], static_cast<uint32_t>(W >> SP_LIMB) & ((1u << SP_LIMB) - 1));
                 atomicAdd(&sm.h.limb[2][bin], static_cast<uint32_t>(W >> (2 * SP_LIMB)));
-            }
-        }
-    }
-    if (LAST) {
-        rest_n = __reduce_add_sync(0xffffffffu, rest_n);
-        if (MASS) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
-        }
-        if (lane == 0 && rest_n) {
-            atomicAdd(&sm.cnt[SP_BINS - 1], rest_n);
-            if (MASS) {
-                atomicAdd(&sm.h.limb[0][SP_BINS - 1], static_cast<uint32_t>(rest) & ((1u << SP_LIMB) - 1));
-                atomicAdd(&sm.h.limb[1][SP_BINS - 1], static_cast<uint32_t>(rest >> SP_LIMB) & ((1u << SP_LIMB) - 1));
-                atomicAdd(&sm.h.limb[2][SP_BINS - 1], static_cast<uint32_t>(rest >> (2 * SP_LIMB)));
             }
         }
     }
@@ -374,9 +412,9 @@ __device__ SpBin select_round(SampleSmem& sm, const SpChunk<TL>& ck, const SpSca
         }
     }
     cluster_sync_all();
-    if (rank == 0) select_bin<MASS>(sm, C, above, cabove, target, frac);
+    if (rank == 0) select_bin<MASS>(sm, C, above, target);
     cluster_sync_all();
-    return SpBin{sm.sel_bin, sm.sel_cnt, sm.sel_cabove, sm.sel_above, sm.sel_total};
+    return SpBin{sm.sel_bin, sm.sel_cnt, sm.sel_above};
 }
 
 // First round: intervals of the logit itself over the 24 binary orders of
@@ -386,48 +424,184 @@ __device__ __forceinline__ SpBins first_bins(const SpScale& sc, float lo) {
     return SpBins{sc.m, width > 0.f && width < 1e30f ? static_cast<float>(SP_BINS - 1) / width : 0.f};
 }
 
-template <typename TL, bool MASS>
-__device__ SpBin select_first(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
-                              float lo, double target, double frac) {
-    const SpBins bins = first_bins(sc, lo);
-    return select_round<TL, MASS, true>(sm, ck, sc, rank, C, 0ull, 0u, target, frac, [&](float l, uint32_t& bin) {
-        bin = bins.of(l);
-        return l >= lo;
-    });
-}
-
-// Later rounds: the ordered keys of one interval, SP_BINS ranges at a time, down
-// to a single key.  Returns that key; `at` becomes its entry.
+// Narrows the intervals b0..b1 (of SpBins over lo) to the ordered key at the
+// border, SP_BINS key ranges at a time; `at` becomes its entry.
 template <typename TL, bool MASS>
 __device__ uint32_t select_key(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
-                               float lo, double target, SpBin& at) {
+                               float lo, uint32_t b0, uint32_t b1, double target, SpBin& at) {
     constexpr int KSH = SpElem<TL>::KSH;
     const SpBins bins = first_bins(sc, lo);
-    const uint32_t b0 = at.b;
-    // bounds of the interval's logits, widened by more than the rounding of SpBins::of
+    // bounds of the intervals' logits, widened by more than the rounding of SpBins::of
     float top = sc.m, bot = lo;
     if (bins.s > 0.f) {
         const float slack = fabsf(sc.m) * 3e-7f;
-        if (b0 > 0) top = fminf(sc.m, sc.m - static_cast<float>(b0) / bins.s * (1.f - 1e-6f) + slack);
-        if (b0 < SP_BINS - 1) bot = fmaxf(lo, sc.m - static_cast<float>(b0 + 1) / bins.s * (1.f + 1e-6f) - slack);
+        if (b0 > 0) top = fminf(sc.m, sc.m - (static_cast<float>(b0) - 0.5f) / bins.s * (1.f - 1e-6f) + slack);
+        bot = bins.lower(b1, lo);
     }
     uint32_t khi = order_key(top) >> KSH, klo = order_key(bot) >> KSH;
-    const unsigned long long total = at.total;
-    while (khi > klo) {
-        int sh = 0;
+    int sh;
+    do {
+        sh = 0;
         while (((khi - klo) >> sh) >= SP_BINS) ++sh;
-        at = select_round<TL, MASS, false>(sm, ck, sc, rank, C, at.above, at.cabove, target, 0.0,
-                                           [&](float l, uint32_t& bin) {
-                                               const uint32_t key = order_key(l) >> KSH;
-                                               bin = (khi - key) >> sh;
-                                               return l >= lo && key >= klo && key <= khi && bins.of(l) == b0;
-                                           });
+        at = select_round<TL, MASS>(sm, ck, sc, rank, C, at.above, target, [&](float l, uint32_t& bin) {
+            const uint32_t key = order_key(l) >> KSH, b = bins.of(l);
+            bin = (khi - key) >> sh;
+            return l >= lo && key >= klo && key <= khi && b >= b0 && b <= b1;
+        });
         khi -= at.b << sh;
         const uint32_t span = (1u << sh) - 1;
         klo = khi - klo > span ? khi - span : klo;
-    }
-    at.total = total;
+    } while (sh > 0);
     return khi;
+}
+
+// Top-k over the whole row: the key of the k-th token.
+template <typename TL>
+__device__ uint32_t select_kth(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
+                               float lo, int k, SpBin& at) {
+    const SpBins bins = first_bins(sc, lo);
+    at = select_round<TL, false>(sm, ck, sc, rank, C, 0ull, static_cast<double>(k), [&](float l, uint32_t& bin) {
+        bin = bins.of(l);
+        return l >= lo;
+    });
+    const uint32_t b = at.b;
+    return select_key<TL, false>(sm, ck, sc, rank, C, lo, b, b, static_cast<double>(k), at);
+}
+
+// Sum of the weights of a vector's elements at or above tau, into two running
+// sums.  A warp that keeps all of its elements sums them without a test, others
+// skip pairs of elements that none of their lanes keeps.
+template <typename TL>
+__device__ __forceinline__ void add_weights(const uint4& r, float tau, typename SpElem<TL>::Bound tb, const SpScale& sc,
+                                            double& s0, double& s1) {
+    constexpr int VEC = SpElem<TL>::VEC;
+    if (__all_sync(0xffffffffu, SpElem<TL>::all_ge(r, tb))) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            s0 += sc.weight(SpElem<TL>::scaled(r, e), sc.tab);
+            s1 += sc.weight(SpElem<TL>::scaled(r, e + 1), sc.tab);
+        }
+    } else if (__any_sync(0xffffffffu, SpElem<TL>::any_ge(r, tb))) {
+        float v[VEC];
+        SpElem<TL>::unpack(r, v);
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const bool in0 = v[e] >= tau, in1 = v[e + 1] >= tau;
+            if (!__any_sync(0xffffffffu, in0 || in1)) continue;
+            const double w0 = sc.weight(v[e]), w1 = sc.weight(v[e + 1]);
+            if (in0) s0 += w0;
+            if (in1) s1 += w1;
+        }
+    }
+}
+
+// Top-p over the elements at or above lo, first step: their sum S (less
+// `minus`), exactly, and from a histogram of counts the intervals b0..b1 that
+// hold the border of the shortest prefix reaching p S.  An interval's tokens
+// weigh between its ends' weights (2^(1/43) apart), so counts bound the running
+// sums from both sides.  Clears nothing: sm.cnt is zero in every CTA when called.
+struct SpNucleus {
+    double S;
+    uint32_t b0, b1, n;   // n: tokens down to b1
+};
+template <typename TL>
+__device__ SpNucleus nucleus(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
+                             float lo, double p, double minus) {
+    constexpr int VEC = SpElem<TL>::VEC;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const SpBins bins = first_bins(sc, lo);
+    int q0, q1;
+    warp_segment(ck.nvec, warp, q0, q1);
+    double s0 = 0.0, s1 = 0.0;
+    uint32_t rest = 0;
+    const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(lo);
+    for (int v0 = q0; v0 < q1; v0 += 32) {
+        const uint4 raw = ck.raw_to(v0 + lane, q1);
+        float v[VEC];
+        SpElem<TL>::unpack(raw, v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            if (!(v[e] >= lo)) continue;
+            const uint32_t b = bins.of(v[e]);
+            if (b == SP_BINS - 1) ++rest;   // the bulk of a peaked row: counted in a register
+            else atomicAdd(&sm.cnt[b], 1u);
+        }
+        add_weights<TL>(raw, lo, tb, sc, s0, s1);
+    }
+    const double s = warp_sum_f64(s0 + s1);
+    rest = __reduce_add_sync(0xffffffffu, rest);
+    if (lane < static_cast<int>(C)) st_cluster_f64(&sm.wsum[rank * SP_WARPS + warp], lane, s);
+    if (lane == 0 && rest) atomicAdd(&sm.cnt[SP_BINS - 1], rest);
+    if (rank != 0) {
+        __syncthreads();
+        for (int i = tid; i < SP_BINS; i += SP_THREADS)
+            if (sm.cnt[i]) red_cluster_u32(&sm.cnt[i], 0, sm.cnt[i]);
+    }
+    cluster_sync_all();
+    SpNucleus r;
+    r.S = table_sum(sm.wsum, C, lane) - minus;
+    if (rank == 0) {
+        const float step = bins.s > 0.f ? static_cast<float>(sc.c) / bins.s : 0.f;   // -log2 of the weight, per interval
+        const double target = fmax(p * r.S, 1e-9);
+        double lo2[SP_BPT], hi2[SP_BPT], hown = 0.0, lown = 0.0;
+        uint32_t n[SP_BPT], nown = 0;
+#pragma unroll
+        for (int j = 0; j < SP_BPT; ++j) {
+            const int b = SP_BPT * tid + j;
+            n[j] = sm.cnt[b];
+            const double cn = static_cast<double>(n[j]);
+            hi2[j] = cn * static_cast<double>(fminf(1.f, exp2f(-step * (static_cast<float>(b) - 0.5f)) * 1.0001f));
+            lo2[j] = b == SP_BINS - 1 || !(bins.s > 0.f) ? 0.0 : cn * static_cast<double>(exp2f(-step * (static_cast<float>(b) + 0.5f)) * 0.9999f);
+            hown += hi2[j];
+            lown += lo2[j];
+            nown += n[j];
+        }
+        const double hinc = warp_scan(hown, lane), linc = warp_scan(lown, lane);
+        const uint32_t ninc = warp_scan(nown, lane);
+        if (lane == 31) {
+            sm.dscan[warp] = hinc;
+            sm.dscan2[warp] = linc;
+            sm.wcnt[warp] = ninc;
+        }
+        if (tid == 0) {
+            sm.nb0 = SP_BINS - 1;
+            sm.nb1 = SP_BINS - 1;
+        }
+        __syncthreads();
+        double h = hinc - hown, l = linc - lown;
+        uint32_t nex = ninc - nown;
+        for (int w = 0; w < warp; ++w) {
+            h += sm.dscan[w];
+            l += sm.dscan2[w];
+            nex += sm.wcnt[w];
+        }
+        uint32_t run[SP_BPT];
+#pragma unroll
+        for (int j = 0; j < SP_BPT; ++j) {
+            h += hi2[j];
+            l += lo2[j];
+            nex += n[j];
+            run[j] = nex;
+            if (h * (1.0 + 1e-9) >= target) atomicMin(&sm.nb0, static_cast<uint32_t>(SP_BPT * tid + j));
+            if (l >= target) atomicMin(&sm.nb1, static_cast<uint32_t>(SP_BPT * tid + j));
+        }
+        __syncthreads();
+        const uint32_t b1 = sm.nb1;
+#pragma unroll
+        for (int j = 0; j < SP_BPT; ++j)
+            if (b1 == static_cast<uint32_t>(SP_BPT * tid + j)) sm.nn = run[j];
+        __syncthreads();
+        if (tid < static_cast<int>(C)) {
+            st_cluster_s32(&sm.nuc[0], tid, static_cast<int>(sm.nb0));
+            st_cluster_s32(&sm.nuc[1], tid, static_cast<int>(sm.nb1));
+            st_cluster_s32(&sm.nuc[2], tid, static_cast<int>(sm.nn));
+        }
+    }
+    cluster_sync_all();
+    r.b0 = sm.nuc[0];
+    r.b1 = sm.nuc[1];
+    r.n = sm.nuc[2];
+    return r;
 }
 
 // The logit that a key stands for.
@@ -437,21 +611,24 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
     return key_value(KSH ? (key << KSH) | ((key >> 15) ? 0u : 0xffffu) : key);
 }
 
-// This CTA's elements that keep() accepts as composite keys in sm.l.loc, in
-// index order, and the count of every CTA in sm.ccnt.  Returns the cluster's
-// count; where it exceeds SP_CAP the lists are not complete.
+// This CTA's elements at or above `floor` that keep() accepts as composite keys
+// in sm.l.loc, in index order, and the count of every CTA in sm.ccnt.  Returns
+// the cluster's count; where it exceeds SP_CAP the lists are not complete.
 template <typename TL, typename F>
-__device__ uint32_t gather(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, F keep) {
+__device__ uint32_t gather(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float floor, F keep) {
     constexpr int VEC = SpElem<TL>::VEC;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
     uint32_t n = 0;
+    const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(floor);
     for (int q = q0 + lane; q < q1; q += 32) {
+        const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[q];
+        if (!SpElem<TL>::any_ge(raw, tb)) continue;
         float v[VEC];
-        ck.load(q, v);
+        SpElem<TL>::unpack(raw, v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) n += keep(v[e]) ? 1u : 0u;
+        for (int e = 0; e < VEC; ++e) n += v[e] >= floor && keep(v[e]) ? 1u : 0u;
     }
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) sm.wcnt[warp] = n;
@@ -466,14 +643,13 @@ __device__ uint32_t gather(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank,
     if (tid < static_cast<int>(C)) st_cluster_s32(&sm.ccnt[rank], tid, static_cast<int>(tot));
     if (tot <= SP_CAP && n > 0) {
         for (int v0 = q0; v0 < q1; v0 += 32) {
+            const uint4 raw = ck.raw_to(v0 + lane, q1);
+            if (!__any_sync(0xffffffffu, SpElem<TL>::any_ge(raw, tb))) continue;
             uint32_t mask = 0;
             float v[VEC];
-            if (v0 + lane < q1) {
-                ck.load(v0 + lane, v);
+            SpElem<TL>::unpack(raw, v);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) mask |= (keep(v[e]) ? 1u : 0u) << e;
-            }
-            if (!__any_sync(0xffffffffu, mask)) continue;
+            for (int e = 0; e < VEC; ++e) mask |= (v[e] >= floor && keep(v[e]) ? 1u : 0u) << e;
             const uint32_t mine = __popc(mask);
             const uint32_t in = warp_scan(mine, lane);
             uint32_t w = at + in - mine;
@@ -497,27 +673,38 @@ __device__ float kth_bound(SampleSmem& sm, const SpScale& sc, uint32_t C, float 
     const SpBins bins = first_bins(sc, lo);
     if (mine >= lo) atomicAdd(&sm.cnt[bins.of(mine)], 1u);   // cleared before the first cluster barrier
     cluster_sync_all();
-    uint32_t n[2] = {0, 0};
+    uint32_t n[SP_BPT], own = 0;
+#pragma unroll
+    for (int j = 0; j < SP_BPT; ++j) n[j] = 0;
 #pragma unroll 8
-    for (uint32_t r = 0; r < C; ++r) {
-        uint32_t x, y;
-        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(sp_mapa(&sm.cnt[2 * tid], r)) : "memory");
-        n[0] += x;
-        n[1] += y;
-    }
+    for (uint32_t r = 0; r < C; ++r)
+#pragma unroll
+        for (int j = 0; j < SP_BPT; j += 2) {
+            uint32_t x, y;
+            asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(x), "=r"(y)
+                         : "r"(sp_mapa(&sm.cnt[SP_BPT * tid + j], r))
+                         : "memory");
+            n[j] += x;
+            n[j + 1] += y;
+        }
     if (tid == 0) sm.last = SP_BINS;
-    const uint32_t own = n[0] + n[1];
+#pragma unroll
+    for (int j = 0; j < SP_BPT; ++j) own += n[j];
     const uint32_t inc = warp_scan(own, lane);
     if (lane == 31) sm.wcnt[warp] = inc;
     __syncthreads();
     uint32_t ex = inc - own;
     for (int w = 0; w < warp; ++w) ex += sm.wcnt[w];
-    if (ex < k && ex + own >= k) sm.last = ex + n[0] >= k ? 2 * tid : 2 * tid + 1;
+#pragma unroll
+    for (int j = 0; j < SP_BPT; ++j) {
+        if (ex < k && ex + n[j] >= k) sm.last = SP_BPT * tid + j;
+        ex += n[j];
+    }
     __syncthreads();
     const int b = sm.last;
     __syncthreads();   // wcnt and last are free again
-    if (b >= SP_BINS - 1 || !(bins.s > 0.f)) return lo;
-    return fmaxf(lo, sc.m - static_cast<float>(b + 1) / bins.s * (1.f + 1e-6f) - fabsf(sc.m) * 3e-7f);
+    return bins.lower(b, lo);
 }
 
 // ---------------------------------------------------------------- the draw from a list (leader)
@@ -545,14 +732,14 @@ __device__ __forceinline__ void block_runs(SampleSmem& sm, double own, int nwarp
 // Descending order of n composite keys from lst into srt.
 __device__ void sort_list(SampleSmem& sm, const unsigned long long* lst, unsigned long long* srt, int n) {
     const int tid = threadIdx.x;
-    if (n <= 128) {   // each key's rank by counting, four threads a key
+    if (n <= 128) {   // each key's rank by counting, SP_THREADS / 128 threads a key
         uint32_t* rk = sm.cnt;
         for (int i = tid; i < 128; i += SP_THREADS) rk[i] = 0;
         __syncthreads();
         const int i = tid & 127, part = tid >> 7;
         if (i < n) {
             const unsigned long long k = lst[i];
-            const int per = (n + 3) / 4;
+            const int per = (n + SP_THREADS / 128 - 1) / (SP_THREADS / 128);
             uint32_t r = 0;
 #pragma unroll 4
             for (int j = part * per; j < min(n, part * per + per); ++j) r += lst[j] > k;
@@ -708,23 +895,34 @@ __device__ void draw_from_list(SampleSmem& sm, int n, const SpScale& sc, const S
 }
 
 // ---------------------------------------------------------------- the draw from the whole row
-// A warp's kept weights in index order; with q, the residual max(w - q S, 0).
+// Sum of every warp's weights at or above tau into sums[cta][warp] of every CTA
+// (one cluster barrier).
 template <typename TL>
-__device__ __forceinline__ double kept_weight(float l, int idx, const SpCut& cut, const SpScale& sc, int skip,
-                                              const float* q, double S) {
-    double w = 0.0;
-    if (cut.keeps(l, idx) && idx != skip) {
-        w = sc.weight(l);
-        if (q) w = fmax(0.0, w - static_cast<double>(__ldg(q + idx)) * S);
-    }
-    return w;
+__device__ void segment_sums(double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float tau,
+                             const SpScale& sc) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int q0, q1;
+    warp_segment(ck.nvec, warp, q0, q1);
+    double s0 = 0.0, s1 = 0.0;
+    const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(tau);
+    for (int v0 = q0; v0 < q1; v0 += 32) add_weights<TL>(ck.raw_to(v0 + lane, q1), tau, tb, sc, s0, s1);
+    const double s = warp_sum_f64(s0 + s1);
+    if (lane < static_cast<int>(C)) st_cluster_f64(&sums[rank * SP_WARPS + warp], lane, s);
+    cluster_sync_all();
 }
 
-// Sum of every warp's kept weights into sums[cta][warp] of every CTA (one
-// cluster barrier).
+// One element of the residual max(w - q S, 0) of the weights at or above tau
+// (q NULL: of the weights).
 template <typename TL>
-__device__ void segment_sums(double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, const SpCut& cut,
-                             const SpScale& sc, int skip, const float* q, double S) {
+__device__ __forceinline__ double left_weight(float l, int idx, float tau, const SpScale& sc, const float* q, double S) {
+    if (!(l >= tau)) return 0.0;
+    const double w = sc.weight(l);
+    return q ? fmax(0.0, w - static_cast<double>(__ldg(q + idx)) * S) : w;
+}
+
+template <typename TL>
+__device__ void residual_sums(double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float tau,
+                              const SpScale& sc, const float* q, double S) {
     constexpr int VEC = SpElem<TL>::VEC;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int q0, q1;
@@ -734,25 +932,18 @@ __device__ void segment_sums(double* sums, const SpChunk<TL>& ck, uint32_t rank,
         float v[VEC];
         ck.load(v0, v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s += kept_weight<TL>(v[e], ck.index(v0, e), cut, sc, skip, q, S);
+        for (int e = 0; e < VEC; ++e) s += left_weight<TL>(v[e], ck.index(v0, e), tau, sc, q, S);
     }
     s = warp_sum_f64(s);
     if (lane < static_cast<int>(C)) st_cluster_f64(&sums[rank * SP_WARPS + warp], lane, s);
     cluster_sync_all();
 }
 
-// Sum of the table, the same in every thread of the cluster.
-__device__ double table_sum(const double* sums, uint32_t C, int lane) {
-    double s = 0.0;
-    for (int i = lane; i < static_cast<int>(C) * SP_WARPS; i += 32) s += sums[i];
-    return warp_sum_f64(s);
-}
-
 // The first index whose cumulative weight exceeds u times the total.  Returns
 // the token in the warp that owns it, -1 elsewhere.
 template <typename TL>
-__device__ int draw_token(const double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, const SpCut& cut,
-                          const SpScale& sc, int skip, const float* q, double S, double u) {
+__device__ int draw_token(const double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float tau,
+                          const SpScale& sc, const float* q, double S, double u) {
     constexpr int VEC = SpElem<TL>::VEC;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nseg = static_cast<int>(C) * SP_WARPS;
@@ -797,17 +988,13 @@ __device__ int draw_token(const double* sums, const SpChunk<TL>& ck, uint32_t ra
         double w[VEC], s = 0.0;
         const int vq = v0 + lane;
         int mine = -1;
+        float v[VEC];
+        ck.load_to(vq, q1, v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = 0.0;
-        if (vq < q1) {
-            float v[VEC];
-            ck.load(vq, v);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                w[e] = kept_weight<TL>(v[e], ck.index(vq, e), cut, sc, skip, q, S);
-                s += w[e];
-                if (w[e] > 0.0) mine = ck.index(vq, e);
-            }
+        for (int e = 0; e < VEC; ++e) {
+            w[e] = left_weight<TL>(v[e], ck.index(vq, e), tau, sc, q, S);
+            s += w[e];
+            if (w[e] > 0.0) mine = ck.index(vq, e);
         }
         const double in = warp_scan(s, lane);
         const unsigned pass = __ballot_sync(0xffffffffu, s > 0.0 && base + in > target);
@@ -884,15 +1071,94 @@ __device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, u
     return static_cast<int>(sm.cut_idx);
 }
 
+// Masks this CTA's elements equal to tau behind index icut.
+template <typename TL>
+__device__ void mask_ties(const SpChunk<TL>& ck, float tau, int icut) {
+    for (int i = max(0, icut + 1 - ck.begin) + threadIdx.x; i < ck.n; i += SP_THREADS)
+        if (static_cast<float>(ck.buf[ck.mis + i]) == tau) ck.buf[ck.mis + i] = SpElem<TL>::ninf();
+}
+
+// Sum of the weights at or above lo in intervals before b0, the same in every
+// thread (one cluster barrier).
+template <typename TL>
+__device__ double above_sum(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float lo,
+                            const SpBins& bins, uint32_t b0, const SpScale& sc) {
+    constexpr int VEC = SpElem<TL>::VEC;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int q0, q1;
+    warp_segment(ck.nvec, warp, q0, q1);
+    double s = 0.0;
+    if (b0 > 0) {
+        const float floor = bins.lower(b0 - 1, lo);
+        const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(floor);
+        for (int v0 = q0; v0 < q1; v0 += 32) {
+            const uint4 raw = ck.raw_to(v0 + lane, q1);
+            if (!__any_sync(0xffffffffu, SpElem<TL>::any_ge(raw, tb))) continue;
+            float v[VEC];
+            SpElem<TL>::unpack(raw, v);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const bool in = v[e] >= floor && bins.of(v[e]) < b0;
+                if (!__any_sync(0xffffffffu, in)) continue;
+                const double w = sc.weight(v[e]);
+                if (in) s += w;
+            }
+        }
+    }
+    s = warp_sum_f64(s);
+    if (lane < static_cast<int>(C)) st_cluster_f64(&sm.rsum[rank * SP_WARPS + warp], lane, s);
+    cluster_sync_all();
+    return table_sum(sm.rsum, C, lane);
+}
+
+// The row's part of probs: w / S in fp32, 0 below tau.
+template <typename TL>
+__device__ void write_probs(float* out, const SpChunk<TL>& ck, float tau, const SpScale& sc, const double* tab) {
+    constexpr int VEC = SpElem<TL>::VEC;
+    const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(tau);
+    const bool wide = ck.mis == 0 && (reinterpret_cast<uintptr_t>(out + ck.begin) & 15u) == 0;
+    const int lane = threadIdx.x & 31;
+    for (int v0 = (threadIdx.x >> 5) * 32; v0 < ck.nvec; v0 += SP_THREADS) {
+        const int vq = v0 + lane;
+        float p[VEC];
+        const uint4 raw = ck.raw_to(vq, ck.nvec);
+        if (__all_sync(0xffffffffu, SpElem<TL>::all_ge(raw, tb))) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) p[e] = static_cast<float>(sc.weight(SpElem<TL>::scaled(raw, e), tab));
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) p[e] = 0.f;
+            if (__any_sync(0xffffffffu, SpElem<TL>::any_ge(raw, tb))) {
+                float v[VEC];
+                SpElem<TL>::unpack(raw, v);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (v[e] >= tau) p[e] = static_cast<float>(sc.weight(SpElem<TL>::scaled(raw, e), tab));
+            }
+        }
+        const int i0 = vq * VEC - ck.mis;   // position in the part
+        if (vq >= ck.nvec) continue;
+        if (wide && i0 + VEC <= ck.n) {
+#pragma unroll
+            for (int e = 0; e < VEC; e += 4)
+                *reinterpret_cast<float4*>(out + ck.begin + i0 + e) = make_float4(p[e], p[e + 1], p[e + 2], p[e + 3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (i0 + e >= 0 && i0 + e < ck.n) out[ck.begin + i0 + e] = p[e];
+        }
+    }
+}
+
 template <typename TL, bool VERIFY>
-__global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(const SampleArgs a) {
     constexpr int VEC = SpElem<TL>::VEC;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ SampleSmem sm;
     const uint32_t rank = cluster_rank(), C = a.cluster;
     const int row = blockIdx.x / a.cluster;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid < 16) sm.tab[tid] = exp2(static_cast<double>(tid) / 16.0);
+    if (tid < 16) sm.tab[tid] = __hiloint2double(__double2hiint(exp2(tid / 16.0)) - (tid << 16), __double2loint(exp2(tid / 16.0)));
     for (int i = tid; i < SP_BINS; i += SP_THREADS) sm.cnt[i] = 0;
     grid_dep_wait();
     grid_dep_launch();
@@ -906,7 +1172,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs 
     const TL* g = rowp + ck.begin;
     ck.mis = static_cast<int>((reinterpret_cast<uintptr_t>(g) & 15u) / sizeof(TL));
     ck.nvec = ck.n > 0 ? (ck.mis + ck.n + VEC - 1) / VEC : 0;
-    float mine = -INFINITY;
+    typename SpElem<TL>::Max tmax;
     for (int q0 = tid; q0 < ck.nvec; q0 += 4 * SP_THREADS) {
         uint4 r[4];
 #pragma unroll
@@ -927,12 +1193,10 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs 
                 memcpy(&r[j], t, 16);
             }
             reinterpret_cast<uint4*>(ck.buf)[q] = r[j];
-            float v[VEC];
-            SpElem<TL>::unpack(r[j], v);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) mine = fmaxf(mine, v[e]);   // a NaN operand is ignored
+            tmax.add(r[j]);   // NaN operands are ignored
         }
     }
+    const float mine = tmax.get();
     float m = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -973,10 +1237,13 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs 
     r.us = static_cast<double>(__ldg(a.u + (VERIFY ? static_cast<size_t>(seq) * a.per + a.per - 1 : static_cast<size_t>(row))));
     r.us = fmin(r.us, 1.0 - 0x1p-24);
 
+    T = fmax(T, 1e-30);
+
     cluster_sync_all();
     m = -INFINITY;
     for (uint32_t i = 0; i < C; ++i) m = fmaxf(m, sm.cmax[i]);
-    const SpScale sc{m, bits_to_f64(__float_as_uint(m)), 1.4426950408889634 / T, sm.tab};
+    const double c = 1.4426950408889634 / T;
+    const SpScale sc{m, scaled_f64(m), c * 0x1p896, c, sm.tab};
     double dmin = -44.361419555836498 * T;   // 64 ln 2
     if (mp > 0.0) dmin = fmax(dmin, T * log(fmin(mp, 1.0)));
     const float lcut = fmaxf(__double2float_ru(static_cast<double>(m) + dmin), -FLT_MAX);
@@ -992,18 +1259,18 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs 
     uint32_t n = 0xffffffffu;
     double S_all = -1.0;
     float list_lo = lcut;
-    SpBin at{};
-    if (mp > 0.0) n = gather<TL>(sm, ck, rank, C, [&](float l) { return l >= lcut; });
+    if (mp > 0.0) n = gather<TL>(sm, ck, rank, C, lcut, [](float) { return true; });
     if (n > SP_CAP && r.by_k && r.k <= SP_CAP) {
         list_lo = kth_bound(sm, sc, C, lcut, mine, static_cast<uint32_t>(r.k));
-        n = gather<TL>(sm, ck, rank, C, [&](float l) { return l >= list_lo; });
+        n = gather<TL>(sm, ck, rank, C, list_lo, [](float) { return true; });
     }
+    SpNucleus nu{};
     if (n > SP_CAP && r.by_p && !r.by_k) {
-        at = select_first<TL, true>(sm, ck, sc, rank, C, lcut, -1.0, r.p);
-        S_all = static_cast<double>(at.total) / static_cast<double>(1ull << SP_FIX);
-        if (at.cabove + at.cnt <= SP_CAP) {
+        nu = nucleus<TL>(sm, ck, sc, rank, C, lcut, r.p, 0.0);
+        S_all = nu.S;
+        if (nu.n <= SP_CAP) {
             const SpBins bins = first_bins(sc, lcut);
-            n = gather<TL>(sm, ck, rank, C, [&](float l) { return l >= lcut && bins.of(l) <= at.b; });
+            n = gather<TL>(sm, ck, rank, C, bins.lower(nu.b1, lcut), [&](float l) { return bins.of(l) <= nu.b1; });
         }
     }
     if (n <= SP_CAP) {
@@ -1030,57 +1297,68 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs 
         cluster_sync_all();
     }
 
-    // ---- many: the border of the kept set by selection over the whole row
-    SpCut cut{lcut, INT_MAX};
+    // ---- many: the border of the kept set by selection over the whole row, then sums and the draw
+    float tau = lcut;              // kept: logits at or above tau; ties that are not are masked
     double S = 0.0;
     if (n <= SP_CAP) {
         S = sm.list_sum;
-        cut.tau = list_lo;   // the whole list is kept where it has no cut
+        tau = list_lo;             // the whole list is kept where it has no cut
         if (sm.list_cut) {
-            cut.tau = composite_value(sm.list_cut);
-            cut.icut = composite_index(sm.list_cut);
+            tau = composite_value(sm.list_cut);
+            mask_ties<TL>(ck, tau, composite_index(sm.list_cut));
+            __syncthreads();
         }
     } else {
         if (r.by_k || r.by_p) {
+            SpBin at{};
             unsigned long long keep = 0;   // how many of the tokens at the border are kept
-            uint32_t key = 0;
-            float lo = lcut;
             if (r.by_k) {
-                at = select_first<TL, false>(sm, ck, sc, rank, C, lcut, static_cast<double>(r.k), 0.0);
-                key = select_key<TL, false>(sm, ck, sc, rank, C, lcut, static_cast<double>(r.k), at);
-                const unsigned long long want = static_cast<unsigned long long>(r.k) - min(at.above, static_cast<unsigned long long>(r.k));
-                keep = min(want, static_cast<unsigned long long>(at.cnt));
-                lo = key_logit<TL>(key);
+                tau = key_logit<TL>(select_kth<TL>(sm, ck, sc, rank, C, lcut, r.k, at));
+                const unsigned long long k = static_cast<unsigned long long>(r.k);
+                keep = min(k - min(at.above, k), static_cast<unsigned long long>(at.cnt));
             }
             if (r.by_p) {
-                const float kth = lo;
+                const float kth = tau;
                 const unsigned long long kkeep = keep;
-                double target;
                 if (r.by_k) {
-                    // the sum over the top-k tokens: everything above the border, and its kept ties
-                    segment_sums<TL>(sm.wsum, ck, rank, C, SpCut{kth, -1}, sc, -1, nullptr, 0.0);
-                    target = fmax(r.p * (table_sum(sm.wsum, C, lane) + static_cast<double>(keep) * sc.weight(kth)), 1e-9);
-                    at = select_first<TL, true>(sm, ck, sc, rank, C, kth, target * static_cast<double>(1ull << SP_FIX), 0.0);
-                } else {
-                    target = fmax(r.p * S_all, 1e-9);
+                    for (int i = tid; i < SP_BINS; i += SP_THREADS) sm.cnt[i] = 0;
+                    cluster_sync_all();
+                    nu = nucleus<TL>(sm, ck, sc, rank, C, kth, r.p,
+                                     static_cast<double>(at.cnt - keep) * sc.weight(kth));
                 }
-                key = select_key<TL, true>(sm, ck, sc, rank, C, lo, target * static_cast<double>(1ull << SP_FIX), at);
-                lo = key_logit<TL>(key);
-                const double need =
-                    ceil((target - static_cast<double>(at.above) / static_cast<double>(1ull << SP_FIX)) / sc.weight(lo));
+                // the border lies in intervals b0..b1: the sum above them exactly, then key by key
+                const double target = fmax(r.p * nu.S, 1e-9);
+                const SpBins bins = first_bins(sc, kth);
+                const double A = above_sum<TL>(sm, ck, rank, C, kth, bins, nu.b0, sc);
+                at.above = static_cast<unsigned long long>(__double2ll_rn(A * static_cast<double>(1ull << SP_FIX)));
+                tau = key_logit<TL>(select_key<TL, true>(sm, ck, sc, rank, C, kth, nu.b0, nu.b1,
+                                                         target * static_cast<double>(1ull << SP_FIX), at));
+                const double need = ceil((target - static_cast<double>(at.above) / static_cast<double>(1ull << SP_FIX)) /
+                                         sc.weight(tau));
                 keep = need < 1.0 ? 1 : need >= static_cast<double>(at.cnt) ? at.cnt : static_cast<unsigned long long>(need);
-                if (r.by_k && lo == kth) keep = min(keep, kkeep);
+                if (r.by_k && tau == kth) keep = min(keep, kkeep);
             }
-            cut.tau = lo;
-            if (keep < at.cnt) cut.icut = tie_index<TL>(sm, ck, rank, C, lo, static_cast<uint32_t>(keep));
+            if (keep < at.cnt) mask_ties<TL>(ck, tau, tie_index<TL>(sm, ck, rank, C, tau, static_cast<uint32_t>(keep)));
         }
-        // ---- sums, acceptance of the draft, the draw
         double wx = 0.0;
-        if (r.x >= 0) wx = kept_weight<TL>(SpElem<TL>::load(rowp + r.x), r.x, cut, sc, -1, nullptr, 0.0);
-        const int skip = r.has_draft && !r.q ? r.x : -1;   // a certain draft leaves the others
-        segment_sums<TL>(sm.wsum, ck, rank, C, cut, sc, skip, nullptr, 0.0);
+        if (r.x >= 0) {
+            __syncthreads();   // masked ties
+            // the draft's weight, where it is kept: from the one CTA that holds it
+            if (tid == 0) {
+                const int i = r.x - ck.begin;
+                if (i >= 0 && i < ck.n) {
+                    const float l = static_cast<float>(ck.buf[ck.mis + i]);
+                    const double w = l >= tau ? sc.weight(l) : 0.0;
+                    for (uint32_t j = 0; j < C; ++j) st_cluster_f64(&sm.wx, j, w);
+                    if (!r.q) ck.mask(r.x);   // a certain draft leaves the others
+                }
+            }
+        }
+        __syncthreads();
+        segment_sums<TL>(sm.wsum, ck, rank, C, tau, sc);
         const double rest = table_sum(sm.wsum, C, lane);
-        S = skip >= 0 ? rest + wx : rest;
+        if (r.x >= 0) wx = sm.wx;
+        S = r.has_draft && !r.q ? rest + wx : rest;
         if (r.has_draft) {
             const double qx = r.q ? (r.x >= 0 ? static_cast<double>(__ldg(r.q + r.x)) : 0.0) : 1.0;
             if (wx > 0.0 && r.ua * qx * S < wx) {
@@ -1090,23 +1368,24 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(const SampleArgs 
         }
         int tok = -1;
         if (r.q) {
-            segment_sums<TL>(sm.rsum, ck, rank, C, cut, sc, -1, r.q, S);
-            if (table_sum(sm.rsum, C, lane) > 0.0) tok = draw_token<TL>(sm.rsum, ck, rank, C, cut, sc, -1, r.q, S, r.us);
-            else tok = draw_token<TL>(sm.wsum, ck, rank, C, cut, sc, -1, nullptr, 0.0, r.us);
+            residual_sums<TL>(sm.rsum, ck, rank, C, tau, sc, r.q, S);
+            if (table_sum(sm.rsum, C, lane) > 0.0) tok = draw_token<TL>(sm.rsum, ck, rank, C, tau, sc, r.q, S, r.us);
+            else tok = draw_token<TL>(sm.wsum, ck, rank, C, tau, sc, nullptr, 0.0, r.us);
         } else if (rest > 0.0) {
-            tok = draw_token<TL>(sm.wsum, ck, rank, C, cut, sc, skip, nullptr, 0.0, r.us);
+            tok = draw_token<TL>(sm.wsum, ck, rank, C, tau, sc, nullptr, 0.0, r.us);
         } else if (rank == 0 && warp == 0) {
             tok = r.x;   // the draft is the only token kept
         }
         if (tok >= 0 && lane == 0) a.token[row] = tok;
     }
     if (!VERIFY && a.probs) {
-        float* out = a.probs + static_cast<size_t>(row) * a.V + ck.begin;
-        const double inv = 1.0 / S;
-        for (int i = tid; i < ck.n; i += SP_THREADS) {
-            const float l = static_cast<float>(ck.buf[ck.mis + i]);
-            out[i] = static_cast<float>(kept_weight<TL>(l, ck.begin + i, cut, sc, -1, nullptr, 0.0) * inv);
+        // 2^(j/16) / S: sums of high words stay within the exponent's range, as probabilities are normal numbers
+        if (tid < 16) {
+            const double x = exp2(tid / 16.0) / S;
+            sm.ptab[tid] = __hiloint2double(__double2hiint(x) - (tid << 16), __double2loint(x));
         }
+        __syncthreads();
+        write_probs<TL>(a.probs + static_cast<size_t>(row) * a.V, ck, tau, sc, sm.ptab);
     }
 }
 
