@@ -30,13 +30,11 @@ namespace ms {
 constexpr int SP_THREADS = 512;
 constexpr int SP_WARPS = SP_THREADS / 32;
 constexpr int SP_MAXC = 8;              // CTAs of a row's cluster
-constexpr int SP_MAX_CHUNK = 32768;     // elements of a row per CTA (bounds the histogram limbs)
+constexpr int SP_MAX_CHUNK = 32768;     // elements of a row per CTA
 constexpr int SP_BINS = 1024;
 constexpr int32_t SP_ACCEPTED = -2;
 constexpr int SP_MAX_V = SP_MAXC * SP_MAX_CHUNK;
-constexpr int SP_FIX = 45;              // fixed point of histogram masses: 2^18 weights of 1 fit 63 bits
-constexpr int SP_LIMB = 15;             // 3 limbs; 2^15 elements x 2^15 fit a 32-bit counter
-constexpr int SP_CAP = 2048;            // candidates of a row that the leader finishes from a list
+constexpr int SP_CAP = 2048;            // candidates that a CTA lists, and that the leader finishes a row from
 constexpr int SP_BPT = SP_BINS / SP_THREADS;   // bins per thread of a bin scan
 
 struct SampleArgs {
@@ -64,19 +62,25 @@ __device__ __forceinline__ void st_cluster_u64(const void* local, uint32_t rank,
 __device__ __forceinline__ void st_cluster_f64(const void* local, uint32_t rank, double v) {
     st_cluster_u64(local, rank, static_cast<unsigned long long>(__double_as_longlong(v)));
 }
-__device__ __forceinline__ void red_cluster_u32(const void* local, uint32_t rank, uint32_t v) {
-    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(sp_mapa(local, rank)), "r"(v) : "memory");
-}
-__device__ __forceinline__ void red_cluster_u64(const void* local, uint32_t rank, unsigned long long v) {
-    asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(sp_mapa(local, rank)), "l"(v) : "memory");
-}
-
 // A float times 2^-896 as a double: its bits shifted into place, without the
 // exponent's bias.  Infinities become +-2^-768 (masked tokens are sorted out by
 // comparisons on the float itself).
 __device__ __forceinline__ double scaled_f64(float l) {
     const int u = __float_as_int(l);
     return __hiloint2double((u >> 3) & static_cast<int>(0x8fffffffu), u << 29);
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The cluster barrier where only warp 0 has stored to other CTAs since the last
+// one (the others' stores to their own CTA's shared memory are ordered by the
+// block barrier): one warp's fence instead of every warp's.
+__device__ __forceinline__ void cluster_sync_warp0() {
+    __syncthreads();
+    if (threadIdx.x < 32) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    cluster_wait();
 }
 
 // Floats in ascending order as unsigned integers (-0 equal to +0).
@@ -218,36 +222,30 @@ struct SpElem<__nv_bfloat16> {
     static __device__ __forceinline__ __nv_bfloat16 ninf() { return __ushort_as_bfloat16(0xff80); }
 };
 
-// Row masses by logit interval, and the candidate lists; never in use together.
 struct SampleSmem {
     double tab[16], ptab[16];                 // 2^(j/16), and the same over the row's sum
     double wsum[SP_MAXC * SP_WARPS];          // every warp's sum, of every CTA of the cluster
     double rsum[SP_MAXC * SP_WARPS];          // the same for the residual
-    double dscan[SP_WARPS], dscan2[SP_WARPS];
+    double dscan[SP_WARPS];
+    float fscan[2][SP_WARPS];
     unsigned long long scan[SP_WARPS];
-    unsigned long long sel_above;             // broadcast results of a selection round
+    unsigned long long sel_key;
+    double sel_before, sel_w;                 // a selection round's border: the sum before it, its weight
     unsigned long long list_cut;              // broadcast results of a list: composite key of the last token kept,
     double list_sum;                          // and the sum of the kept weights
     double wx;
-    union {
-        struct {
-            unsigned long long mass[SP_BINS];   // leader: masses pushed by the other CTAs
-            uint32_t limb[3][SP_BINS];
-        } h;
-        struct {
-            unsigned long long lst[SP_CAP];     // leader: the row's candidates in index order
-            unsigned long long loc[SP_CAP];     // this CTA's candidates; leader, later: the list in descending order
-        } l;
-    };
-    uint32_t cnt[SP_BINS];
-    float cmax[SP_MAXC];
-    uint32_t ccnt[SP_MAXC];
+    unsigned long long lst[SP_CAP];           // leader: the row's candidates in index order
+    unsigned long long loc[SP_CAP];           // this CTA's candidates; leader, later: scratch for sorting
+    uint32_t cnt[SP_BINS + 31];               // counts by interval; the last interval's in 32 parts, one per lane
+    float cmax[SP_MAXC], cmin[SP_MAXC];       // every CTA's maximum, and the least of its threads' maxima
+    uint32_t ccnt[4][SP_MAXC];                // every CTA's count, of each of up to four gathers
     uint32_t tie[SP_MAXC];
-    float wmax[SP_WARPS];
+    float wmax[SP_WARPS], wmin[SP_WARPS];
+    uint16_t order[SP_CAP];                   // leader: list entries by bucket
     uint32_t wcnt[SP_WARPS];
-    uint32_t sel_bin, sel_cnt;
-    uint32_t nb0, nb1, nn;                    // leader: the top-p border's intervals, and the tokens down to them
-    uint32_t nuc[3];                          // the same, broadcast
+    uint32_t sel_cnt;
+    uint32_t nb0, nb1, nn;                    // the border's intervals and their tokens
+    uint32_t dropped;                         // ties behind the border
     uint32_t cut_idx;                         // broadcast: index of the last tied token kept
     int last;
     uint32_t keep;
@@ -295,6 +293,20 @@ __device__ __forceinline__ void warp_segment(int nvec, int warp, int& q0, int& q
     q1 = min(nvec, q0 + per);
 }
 
+// This CTA's warp sums into row `rank` of the table of every CTA (one cluster
+// barrier).
+__device__ void share_sums(double* sums, double s, uint32_t rank, uint32_t C) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    s = warp_sum_f64(s);
+    double* own = sums + rank * SP_WARPS;
+    if (lane == 0) own[warp] = s;
+    __syncthreads();
+    if (warp == 0)
+        for (int i = lane; i < static_cast<int>(C) * SP_WARPS; i += 32)
+            if (static_cast<uint32_t>(i) / SP_WARPS != rank) st_cluster_f64(own + i % SP_WARPS, i / SP_WARPS, own[i % SP_WARPS]);
+    cluster_sync_warp0();
+}
+
 // Sum of the table, the same in every thread of the cluster.
 __device__ double table_sum(const double* sums, uint32_t C, int lane) {
     double s = 0.0;
@@ -306,166 +318,30 @@ __device__ double table_sum(const double* sums, uint32_t C, int lane) {
 // Logit intervals of equal width below the maximum; the last one takes the rest.
 struct SpBins {
     float m, s;
+    // a bound above every logit of intervals b and later
+    __device__ __forceinline__ float upper(uint32_t b) const {
+        if (b == 0 || !(s > 0.f)) return m;
+        return fminf(m, m - (static_cast<float>(b) - 0.5f) / s * (1.f - 1e-6f) + fabsf(m) * 3e-7f);
+    }
     // a bound below every logit of intervals 0..b that is at least lo, by more than the rounding of of()
     __device__ __forceinline__ float lower(uint32_t b, float lo) const {
         if (b >= SP_BINS - 1 || !(s > 0.f)) return lo;
         return fmaxf(lo, m - (static_cast<float>(b) + 0.5f) / s * (1.f + 1e-6f) - fabsf(m) * 3e-7f);
     }
+    __device__ __forceinline__ uint32_t raw(float l) const {
+        return __float_as_uint(fmaf(m - l, s, 8388608.f)) - 0x4b000000u;
+    }
     __device__ __forceinline__ uint32_t of(float l) const {
         // adding 2^23 leaves the rounded product in the low bits; infinities and NaN (inf - inf) end in the last one
-        return min(__float_as_uint(fmaf(m - l, s, 8388608.f)) - 0x4b000000u, static_cast<uint32_t>(SP_BINS - 1));
+        return min(raw(l), static_cast<uint32_t>(SP_BINS - 1));
     }
 };
-
-struct SpBin {
-    uint32_t b, cnt;            // the interval, and its tokens
-    unsigned long long above;   // mass (or count) above it
-};
-
-// The leader's part of a selection round: merges the tables, scans them from
-// the top and broadcasts the first interval where `above` + the running total
-// reaches the target.
-template <bool MASS>
-__device__ void select_bin(SampleSmem& sm, uint32_t C, unsigned long long above, double target) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned long long v[SP_BPT], own = 0;
-    uint32_t n[SP_BPT];
-#pragma unroll
-    for (int j = 0; j < SP_BPT; ++j) {
-        const int i = SP_BPT * tid + j;
-        n[j] = sm.cnt[i];
-        v[j] = n[j];
-        if (MASS)
-            v[j] = sm.h.mass[i] + sm.h.limb[0][i] + (static_cast<unsigned long long>(sm.h.limb[1][i]) << SP_LIMB) +
-                   (static_cast<unsigned long long>(sm.h.limb[2][i]) << (2 * SP_LIMB));
-        if (n[j]) atomicMax(&sm.last, i);
-        own += v[j];
-    }
-    const unsigned long long inc = warp_scan(own, lane);
-    if (lane == 31) sm.scan[warp] = inc;
-    __syncthreads();
-    unsigned long long ex = above + inc - own, tot = above;
-    for (int w = 0; w < SP_WARPS; ++w) {
-        if (w < warp) ex += sm.scan[w];
-        tot += sm.scan[w];
-    }
-    // the last occupied interval where rounding left the target above the total
-    const bool never = static_cast<double>(tot) < target;
-#pragma unroll
-    for (int j = 0; j < SP_BPT; ++j) {
-        const bool hit = never ? SP_BPT * tid + j == sm.last
-                               : n[j] && static_cast<double>(ex) < target && static_cast<double>(ex + v[j]) >= target;
-        if (hit)
-            for (uint32_t r = 0; r < C; ++r) {
-                st_cluster_s32(&sm.sel_bin, r, SP_BPT * tid + j);
-                st_cluster_s32(&sm.sel_cnt, r, static_cast<int>(n[j]));
-                st_cluster_u64(&sm.sel_above, r, ex);
-            }
-        ex += v[j];
-    }
-}
-
-// One selection round over the cluster's part of the row: a histogram of the
-// elements that bin_of() accepts (counts always, fixed-point masses when MASS),
-// merged and scanned by the leader.
-template <typename TL, bool MASS, typename F>
-__device__ SpBin select_round(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
-                              unsigned long long above, double target, F bin_of) {
-    constexpr int VEC = SpElem<TL>::VEC;
-    const int tid = threadIdx.x;
-    for (int i = tid; i < SP_BINS; i += SP_THREADS) {
-        sm.cnt[i] = 0;
-        if (MASS) {
-            sm.h.limb[0][i] = sm.h.limb[1][i] = sm.h.limb[2][i] = 0;
-            sm.h.mass[i] = 0;
-        }
-    }
-    if (tid == 0) sm.last = 0;
-    cluster_sync_all();   // the leader's tables are clear before anyone adds to them
-    for (int q = tid; q < ck.nvec; q += SP_THREADS) {
-        float v[VEC];
-        ck.load(q, v);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            uint32_t bin;
-            if (!bin_of(v[e], bin)) continue;
-            atomicAdd(&sm.cnt[bin], 1u);
-            if (MASS) {
-                // adding 2^7 leaves the weight as an integer of 2^-45 in the low mantissa bits
-                const double z = sc.weight(v[e]) + 128.0;
-                const unsigned long long W = static_cast<unsigned long long>(__double_as_longlong(z)) & 0xfffffffffffffull;
-                atomicAdd(&sm.h.limb[0][bin], static_cast<uint32_t>(W) & ((1u << SP_LIMB) - 1));
-                atomicAdd(&sm.h.limb[1][bin], static_cast<uint32_t>(W >> SP_LIMB) & ((1u << SP_LIMB) - 1));
-                atomicAdd(&sm.h.limb[2][bin], static_cast<uint32_t>(W >> (2 * SP_LIMB)));
-            }
-        }
-    }
-    __syncthreads();
-    if (rank != 0) {
-        for (int i = tid; i < SP_BINS; i += SP_THREADS) {
-            if (sm.cnt[i] == 0) continue;
-            if (MASS)
-                red_cluster_u64(&sm.h.mass[i], 0,
-                                sm.h.limb[0][i] + (static_cast<unsigned long long>(sm.h.limb[1][i]) << SP_LIMB) +
-                                    (static_cast<unsigned long long>(sm.h.limb[2][i]) << (2 * SP_LIMB)));
-            red_cluster_u32(&sm.cnt[i], 0, sm.cnt[i]);
-        }
-    }
-    cluster_sync_all();
-    if (rank == 0) select_bin<MASS>(sm, C, above, target);
-    cluster_sync_all();
-    return SpBin{sm.sel_bin, sm.sel_cnt, sm.sel_above};
-}
 
 // First round: intervals of the logit itself over the 24 binary orders of
 // magnitude below the largest weight, or down to `lo` where that is nearer.
 __device__ __forceinline__ SpBins first_bins(const SpScale& sc, float lo) {
     const float width = fminf(sc.m - lo, static_cast<float>(24.0 / sc.c));
     return SpBins{sc.m, width > 0.f && width < 1e30f ? static_cast<float>(SP_BINS - 1) / width : 0.f};
-}
-
-// Narrows the intervals b0..b1 (of SpBins over lo) to the ordered key at the
-// border, SP_BINS key ranges at a time; `at` becomes its entry.
-template <typename TL, bool MASS>
-__device__ uint32_t select_key(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
-                               float lo, uint32_t b0, uint32_t b1, double target, SpBin& at) {
-    constexpr int KSH = SpElem<TL>::KSH;
-    const SpBins bins = first_bins(sc, lo);
-    // bounds of the intervals' logits, widened by more than the rounding of SpBins::of
-    float top = sc.m, bot = lo;
-    if (bins.s > 0.f) {
-        const float slack = fabsf(sc.m) * 3e-7f;
-        if (b0 > 0) top = fminf(sc.m, sc.m - (static_cast<float>(b0) - 0.5f) / bins.s * (1.f - 1e-6f) + slack);
-        bot = bins.lower(b1, lo);
-    }
-    uint32_t khi = order_key(top) >> KSH, klo = order_key(bot) >> KSH;
-    int sh;
-    do {
-        sh = 0;
-        while (((khi - klo) >> sh) >= SP_BINS) ++sh;
-        at = select_round<TL, MASS>(sm, ck, sc, rank, C, at.above, target, [&](float l, uint32_t& bin) {
-            const uint32_t key = order_key(l) >> KSH, b = bins.of(l);
-            bin = (khi - key) >> sh;
-            return l >= lo && key >= klo && key <= khi && b >= b0 && b <= b1;
-        });
-        khi -= at.b << sh;
-        const uint32_t span = (1u << sh) - 1;
-        klo = khi - klo > span ? khi - span : klo;
-    } while (sh > 0);
-    return khi;
-}
-
-// Top-k over the whole row: the key of the k-th token.
-template <typename TL>
-__device__ uint32_t select_kth(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
-                               float lo, int k, SpBin& at) {
-    const SpBins bins = first_bins(sc, lo);
-    at = select_round<TL, false>(sm, ck, sc, rank, C, 0ull, static_cast<double>(k), [&](float l, uint32_t& bin) {
-        bin = bins.of(l);
-        return l >= lo;
-    });
-    const uint32_t b = at.b;
-    return select_key<TL, false>(sm, ck, sc, rank, C, lo, b, b, static_cast<double>(k), at);
 }
 
 // Sum of the weights of a vector's elements at or above tau, into two running
@@ -495,6 +371,44 @@ __device__ __forceinline__ void add_weights(const uint4& r, float tau, typename 
     }
 }
 
+// This thread's bins of the cluster's count table, summed over the CTAs.
+__device__ __forceinline__ void pull_counts(SampleSmem& sm, uint32_t C, uint32_t (&n)[SP_BPT]) {
+#pragma unroll
+    for (int j = 0; j < SP_BPT; ++j) n[j] = 0;
+#pragma unroll 8
+    for (uint32_t r = 0; r < C; ++r)
+#pragma unroll
+        for (int j = 0; j < SP_BPT; j += 2) {
+            uint32_t x, y;
+            asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(x), "=r"(y)
+                         : "r"(sp_mapa(&sm.cnt[SP_BPT * threadIdx.x + j], r))
+                         : "memory");
+            n[j] += x;
+            n[j + 1] += y;
+        }
+}
+
+// Counts a vector's elements at or above lo by interval.  The last interval
+// takes the bulk of a peaked row: each lane counts it in a word of its own.
+template <typename TL>
+__device__ __forceinline__ void count_vector(SampleSmem& sm, const uint4& raw, float lo, const SpBins& bins, uint32_t most) {
+    float v[SpElem<TL>::VEC];
+    SpElem<TL>::unpack(raw, v);
+#pragma unroll
+    for (int e = 0; e < SpElem<TL>::VEC; ++e) {
+        const uint32_t b = min(bins.raw(v[e]), most);
+        if (v[e] >= lo) atomicAdd(&sm.cnt[b], 1u);
+    }
+}
+// The last interval's parts as one count (between block barriers).
+__device__ __forceinline__ void join_last(SampleSmem& sm) {
+    if (threadIdx.x < 32) {
+        const uint32_t n = __reduce_add_sync(0xffffffffu, sm.cnt[SP_BINS - 1 + threadIdx.x]);
+        if (threadIdx.x == 0) sm.cnt[SP_BINS - 1] = n;
+    }
+}
+
 // Top-p over the elements at or above lo, first step: their sum S (less
 // `minus`), exactly, and from a histogram of counts the intervals b0..b1 that
 // hold the border of the shortest prefix reaching p S.  An interval's tokens
@@ -507,101 +421,125 @@ struct SpNucleus {
 template <typename TL>
 __device__ SpNucleus nucleus(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
                              float lo, double p, double minus) {
-    constexpr int VEC = SpElem<TL>::VEC;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const SpBins bins = first_bins(sc, lo);
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
     double s0 = 0.0, s1 = 0.0;
-    uint32_t rest = 0;
     const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(lo);
     for (int v0 = q0; v0 < q1; v0 += 32) {
         const uint4 raw = ck.raw_to(v0 + lane, q1);
-        float v[VEC];
-        SpElem<TL>::unpack(raw, v);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            if (!(v[e] >= lo)) continue;
-            const uint32_t b = bins.of(v[e]);
-            if (b == SP_BINS - 1) ++rest;   // the bulk of a peaked row: counted in a register
-            else atomicAdd(&sm.cnt[b], 1u);
-        }
+        count_vector<TL>(sm, raw, lo, bins, SP_BINS - 1 + lane);
         add_weights<TL>(raw, lo, tb, sc, s0, s1);
     }
-    const double s = warp_sum_f64(s0 + s1);
-    rest = __reduce_add_sync(0xffffffffu, rest);
-    if (lane < static_cast<int>(C)) st_cluster_f64(&sm.wsum[rank * SP_WARPS + warp], lane, s);
-    if (lane == 0 && rest) atomicAdd(&sm.cnt[SP_BINS - 1], rest);
-    if (rank != 0) {
-        __syncthreads();
-        for (int i = tid; i < SP_BINS; i += SP_THREADS)
-            if (sm.cnt[i]) red_cluster_u32(&sm.cnt[i], 0, sm.cnt[i]);
-    }
-    cluster_sync_all();
+    __syncthreads();
+    join_last(sm);
+    share_sums(sm.wsum, s0 + s1, rank, C);
     SpNucleus r;
     r.S = table_sum(sm.wsum, C, lane) - minus;
-    if (rank == 0) {
-        const float step = bins.s > 0.f ? static_cast<float>(sc.c) / bins.s : 0.f;   // -log2 of the weight, per interval
-        const double target = fmax(p * r.S, 1e-9);
-        double lo2[SP_BPT], hi2[SP_BPT], hown = 0.0, lown = 0.0;
-        uint32_t n[SP_BPT], nown = 0;
+    // every CTA evaluates the whole table; the margins of 1e-4 cover fp32 sums and exp2f
+    const float step = bins.s > 0.f ? static_cast<float>(sc.c) / bins.s : 0.f;   // -log2 of the weight, per interval
+    const float target = static_cast<float>(fmax(p * r.S, 1e-9));
+    uint32_t n[SP_BPT], nown = 0;
+    pull_counts(sm, C, n);
+    float lo2[SP_BPT], hi2[SP_BPT], hown = 0.f, lown = 0.f;
 #pragma unroll
-        for (int j = 0; j < SP_BPT; ++j) {
-            const int b = SP_BPT * tid + j;
-            n[j] = sm.cnt[b];
-            const double cn = static_cast<double>(n[j]);
-            hi2[j] = cn * static_cast<double>(fminf(1.f, exp2f(-step * (static_cast<float>(b) - 0.5f)) * 1.0001f));
-            lo2[j] = b == SP_BINS - 1 || !(bins.s > 0.f) ? 0.0 : cn * static_cast<double>(exp2f(-step * (static_cast<float>(b) + 0.5f)) * 0.9999f);
-            hown += hi2[j];
-            lown += lo2[j];
-            nown += n[j];
-        }
-        const double hinc = warp_scan(hown, lane), linc = warp_scan(lown, lane);
-        const uint32_t ninc = warp_scan(nown, lane);
-        if (lane == 31) {
-            sm.dscan[warp] = hinc;
-            sm.dscan2[warp] = linc;
-            sm.wcnt[warp] = ninc;
-        }
-        if (tid == 0) {
-            sm.nb0 = SP_BINS - 1;
-            sm.nb1 = SP_BINS - 1;
-        }
-        __syncthreads();
-        double h = hinc - hown, l = linc - lown;
-        uint32_t nex = ninc - nown;
-        for (int w = 0; w < warp; ++w) {
-            h += sm.dscan[w];
-            l += sm.dscan2[w];
-            nex += sm.wcnt[w];
-        }
-        uint32_t run[SP_BPT];
-#pragma unroll
-        for (int j = 0; j < SP_BPT; ++j) {
-            h += hi2[j];
-            l += lo2[j];
-            nex += n[j];
-            run[j] = nex;
-            if (h * (1.0 + 1e-9) >= target) atomicMin(&sm.nb0, static_cast<uint32_t>(SP_BPT * tid + j));
-            if (l >= target) atomicMin(&sm.nb1, static_cast<uint32_t>(SP_BPT * tid + j));
-        }
-        __syncthreads();
-        const uint32_t b1 = sm.nb1;
-#pragma unroll
-        for (int j = 0; j < SP_BPT; ++j)
-            if (b1 == static_cast<uint32_t>(SP_BPT * tid + j)) sm.nn = run[j];
-        __syncthreads();
-        if (tid < static_cast<int>(C)) {
-            st_cluster_s32(&sm.nuc[0], tid, static_cast<int>(sm.nb0));
-            st_cluster_s32(&sm.nuc[1], tid, static_cast<int>(sm.nb1));
-            st_cluster_s32(&sm.nuc[2], tid, static_cast<int>(sm.nn));
-        }
+    for (int j = 0; j < SP_BPT; ++j) {
+        const int b = SP_BPT * tid + j;
+        const float cn = static_cast<float>(n[j]);
+        hi2[j] = cn * fminf(1.f, exp2f(-step * (static_cast<float>(b) - 0.5f))) * 1.0001f;
+        lo2[j] = b == SP_BINS - 1 || !(bins.s > 0.f) ? 0.f : cn * exp2f(-step * (static_cast<float>(b) + 0.5f)) * 0.9999f;
+        hown += hi2[j];
+        lown += lo2[j];
+        nown += n[j];
     }
-    cluster_sync_all();
-    r.b0 = sm.nuc[0];
-    r.b1 = sm.nuc[1];
-    r.n = sm.nuc[2];
+    float h = warp_scan(hown, lane), l = warp_scan(lown, lane);
+    uint32_t nex = warp_scan(nown, lane);
+    if (lane == 31) {
+        sm.fscan[0][warp] = h;
+        sm.fscan[1][warp] = l;
+        sm.wcnt[warp] = nex;
+    }
+    if (tid == 0) {
+        sm.nb0 = SP_BINS - 1;
+        sm.nb1 = SP_BINS - 1;
+    }
+    h -= hown;
+    l -= lown;
+    nex -= nown;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) {
+        h += sm.fscan[0][w];
+        l += sm.fscan[1][w];
+        nex += sm.wcnt[w];
+    }
+    uint32_t f0 = SP_BINS - 1, f1 = SP_BINS - 1, run[SP_BPT];
+#pragma unroll
+    for (int j = 0; j < SP_BPT; ++j) {
+        h += hi2[j];
+        l += lo2[j];
+        nex += n[j];
+        run[j] = nex;
+        if (h >= target) f0 = min(f0, static_cast<uint32_t>(SP_BPT * tid + j));
+        if (l >= target) f1 = min(f1, static_cast<uint32_t>(SP_BPT * tid + j));
+    }
+    f0 = __reduce_min_sync(0xffffffffu, f0);
+    f1 = __reduce_min_sync(0xffffffffu, f1);
+    if (lane == 0) {
+        atomicMin(&sm.nb0, f0);
+        atomicMin(&sm.nb1, f1);
+    }
+    __syncthreads();
+    r.b0 = sm.nb0;
+    r.b1 = sm.nb1;
+#pragma unroll
+    for (int j = 0; j < SP_BPT; ++j)
+        if (r.b1 == static_cast<uint32_t>(SP_BPT * tid + j)) sm.nn = run[j];
+    __syncthreads();
+    r.n = sm.nn;
     return r;
+}
+
+// Top-k over the elements at or above lo, first step: the interval that holds
+// the k-th (the last one where there are fewer), and the tokens above it.
+// Clears nothing: sm.cnt is zero in every CTA when called.
+struct SpKth {
+    uint32_t b, above, cnt;
+};
+template <typename TL>
+__device__ SpKth kth_interval(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t C, float lo,
+                              uint32_t k) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const SpBins bins = first_bins(sc, lo);
+    for (int q = tid; q < ck.nvec; q += SP_THREADS)
+        count_vector<TL>(sm, reinterpret_cast<const uint4*>(ck.buf)[q], lo, bins, SP_BINS - 1 + lane);
+    __syncthreads();
+    join_last(sm);
+    cluster_sync_warp0();
+    uint32_t n[SP_BPT], own = 0;
+    pull_counts(sm, C, n);
+#pragma unroll
+    for (int j = 0; j < SP_BPT; ++j) own += n[j];
+    const uint32_t inc = warp_scan(own, lane);
+    if (lane == 31) sm.wcnt[warp] = inc;
+    __syncthreads();
+    uint32_t ex = inc - own, tot = 0;
+    for (int w = 0; w < SP_WARPS; ++w) {
+        if (w < warp) ex += sm.wcnt[w];
+        tot += sm.wcnt[w];
+    }
+    k = min(k, tot);
+#pragma unroll
+    for (int j = 0; j < SP_BPT; ++j) {
+        if (ex < k && ex + n[j] >= k) {
+            sm.nb0 = SP_BPT * tid + j;
+            sm.nb1 = ex;
+            sm.nn = n[j];
+        }
+        ex += n[j];
+    }
+    __syncthreads();
+    return SpKth{sm.nb0, sm.nb1, sm.nn};
 }
 
 // The logit that a key stands for.
@@ -612,10 +550,12 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
 }
 
 // This CTA's elements at or above `floor` that keep() accepts as composite keys
-// in sm.l.loc, in index order, and the count of every CTA in sm.ccnt.  Returns
-// the cluster's count; where it exceeds SP_CAP the lists are not complete.
+// in sm.loc, in index order, and the count of every CTA in ccnt (not used
+// before).  Returns the cluster's count; a CTA with more than SP_CAP lists none.
+// This warp's entries are loc[start, start + count).
 template <typename TL, typename F>
-__device__ uint32_t gather(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float floor, F keep) {
+__device__ uint32_t gather(SampleSmem& sm, uint32_t* ccnt, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float floor,
+                           F keep, uint32_t* start = nullptr, uint32_t* count = nullptr) {
     constexpr int VEC = SpElem<TL>::VEC;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int q0, q1;
@@ -640,7 +580,11 @@ __device__ uint32_t gather(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank,
         if (w < warp) at += x;
         tot += x;
     }
-    if (tid < static_cast<int>(C)) st_cluster_s32(&sm.ccnt[rank], tid, static_cast<int>(tot));
+    if (tid < static_cast<int>(C)) st_cluster_s32(&ccnt[rank], tid, static_cast<int>(tot));
+    if (start) {
+        *start = at;
+        *count = n;
+    }
     if (tot <= SP_CAP && n > 0) {
         for (int v0 = q0; v0 < q1; v0 += 32) {
             const uint4 raw = ck.raw_to(v0 + lane, q1);
@@ -655,39 +599,30 @@ __device__ uint32_t gather(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank,
             uint32_t w = at + in - mine;
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                if (mask & (1u << e)) sm.l.loc[w++] = composite(v[e], ck.index(v0 + lane, e));
+                if (mask & (1u << e)) sm.loc[w++] = composite(v[e], ck.index(v0 + lane, e));
             at += __shfl_sync(0xffffffffu, in, 31);
         }
     }
-    cluster_sync_all();
+    cluster_sync_warp0();
     uint32_t all = 0;
-    for (uint32_t r = 0; r < C; ++r) all += sm.ccnt[r];
+    for (uint32_t r = 0; r < C; ++r) all += ccnt[r];
     return all;
 }
 
-// A lower bound of the k-th largest logit: the k-th largest of the threads'
-// maxima (each of k threads holds an element at least that large), to within
-// an interval.  -inf where fewer than k threads hold an element above lo.
-__device__ float kth_bound(SampleSmem& sm, const SpScale& sc, uint32_t C, float lo, float mine, uint32_t k) {
+// A lower bound of the k-th largest of the elements at or above lo: the k-th
+// largest of the threads' maxima (each of k threads holds an element at least
+// that large), to within one of SP_BINS intervals between low and high, the
+// least and the largest of those maxima.  lo where fewer than k threads hold an
+// element that large.
+__device__ float kth_bound(SampleSmem& sm, uint32_t C, float lo, float low, float high, float mine, uint32_t k) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const SpBins bins = first_bins(sc, lo);
-    if (mine >= lo) atomicAdd(&sm.cnt[bins.of(mine)], 1u);   // cleared before the first cluster barrier
-    cluster_sync_all();
+    low = fmaxf(low, lo);
+    const float width = high - low;
+    const SpBins bins{high, width > 0.f && width < 1e30f ? static_cast<float>(SP_BINS - 1) / width : 0.f};
+    if (mine >= lo) atomicAdd(&sm.cnt[bins.of(mine)], 1u);   // the table is clear when called
+    cluster_sync_warp0();
     uint32_t n[SP_BPT], own = 0;
-#pragma unroll
-    for (int j = 0; j < SP_BPT; ++j) n[j] = 0;
-#pragma unroll 8
-    for (uint32_t r = 0; r < C; ++r)
-#pragma unroll
-        for (int j = 0; j < SP_BPT; j += 2) {
-            uint32_t x, y;
-            asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
-                         : "=r"(x), "=r"(y)
-                         : "r"(sp_mapa(&sm.cnt[SP_BPT * tid + j], r))
-                         : "memory");
-            n[j] += x;
-            n[j + 1] += y;
-        }
+    pull_counts(sm, C, n);
     if (tid == 0) sm.last = SP_BINS;
 #pragma unroll
     for (int j = 0; j < SP_BPT; ++j) own += n[j];
@@ -704,6 +639,7 @@ __device__ float kth_bound(SampleSmem& sm, const SpScale& sc, uint32_t C, float 
     __syncthreads();
     const int b = sm.last;
     __syncthreads();   // wcnt and last are free again
+    if (b == SP_BINS - 1 && bins.s > 0.f) return low;   // all of the maxima
     return bins.lower(b, lo);
 }
 
@@ -729,6 +665,8 @@ __device__ __forceinline__ void block_runs(SampleSmem& sm, double own, int nwarp
     total = sum;
 }
 
+constexpr int SP_PER = SP_CAP / SP_THREADS;
+
 // Descending order of n composite keys from lst into srt.
 __device__ void sort_list(SampleSmem& sm, const unsigned long long* lst, unsigned long long* srt, int n) {
     const int tid = threadIdx.x;
@@ -750,6 +688,76 @@ __device__ void sort_list(SampleSmem& sm, const unsigned long long* lst, unsigne
         __syncthreads();
         return;
     }
+    // into SP_BINS buckets by logit, then each key's rank within its bucket
+    const int lane = tid & 31, warp = tid >> 5;
+    unsigned long long k[SP_PER];
+    uint32_t least = 0xffffffffu, most = 0;
+#pragma unroll
+    for (int e = 0; e < SP_PER; ++e) {
+        const int i = tid + e * SP_THREADS;
+        k[e] = i < n ? lst[i] : 0ull;
+        if (i < n) {
+            least = min(least, static_cast<uint32_t>(k[e] >> 32));
+            most = max(most, static_cast<uint32_t>(k[e] >> 32));
+        }
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+        sm.wcnt[warp] = least;
+        sm.scan[warp] = most;
+    }
+    for (int i = tid; i < SP_BINS; i += SP_THREADS) sm.cnt[i] = 0;
+    __syncthreads();
+    for (int w = 0; w < SP_WARPS; ++w) {
+        least = min(least, sm.wcnt[w]);
+        most = max(most, static_cast<uint32_t>(sm.scan[w]));
+    }
+    const float high = key_value(most), width = high - key_value(least);
+    const SpBins bins{high, width > 0.f && width < 1e30f ? static_cast<float>(SP_BINS - 1) / width : 0.f};
+    uint32_t b[SP_PER], at[SP_PER];
+#pragma unroll
+    for (int e = 0; e < SP_PER; ++e) {
+        if (tid + e * SP_THREADS >= n) continue;
+        b[e] = bins.of(key_value(static_cast<uint32_t>(k[e] >> 32)));
+        at[e] = atomicAdd(&sm.cnt[b[e]], 1u);
+    }
+    __syncthreads();
+    uint32_t c[SP_BPT], own = 0, big = 0;
+#pragma unroll
+    for (int j = 0; j < SP_BPT; ++j) {
+        c[j] = sm.cnt[SP_BPT * tid + j];
+        own += c[j];
+        big = max(big, c[j]);
+    }
+    const uint32_t inc = warp_scan(own, lane);
+    if (lane == 31) sm.wcnt[warp] = inc;
+    const bool crowded = __syncthreads_or(big > 96);   // (a barrier either way)
+    if (!crowded) {
+        uint32_t ex = inc - own;
+        for (int w = 0; w < warp; ++w) ex += sm.wcnt[w];
+#pragma unroll
+        for (int j = 0; j < SP_BPT; ++j) {
+            sm.cnt[SP_BPT * tid + j] = ex;
+            ex += c[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < SP_PER; ++e)
+            if (tid + e * SP_THREADS < n) sm.order[sm.cnt[b[e]] + at[e]] = static_cast<uint16_t>(tid + e * SP_THREADS);
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < SP_PER; ++e) {
+            if (tid + e * SP_THREADS >= n) continue;
+            const uint32_t i0 = sm.cnt[b[e]], i1 = b[e] + 1 < SP_BINS ? sm.cnt[b[e] + 1] : static_cast<uint32_t>(n);
+            uint32_t r = i0;
+            for (uint32_t i = i0; i < i1; ++i) r += lst[sm.order[i]] > k[e];
+            srt[r] = k[e];
+        }
+        __syncthreads();
+        return;
+    }
+    // many equal logits: a bitonic network
     int p2 = 256;
     while (p2 < n) p2 *= 2;
     for (int i = tid; i < p2; i += SP_THREADS) srt[i] = i < n ? lst[i] : 0ull;
@@ -769,8 +777,6 @@ __device__ void sort_list(SampleSmem& sm, const unsigned long long* lst, unsigne
         }
 }
 
-constexpr int SP_PER = SP_CAP / SP_THREADS;
-
 // Index of the entry of the list where the running sum of w (this thread's
 // run starts at `start`) passes the target, in the one thread it falls to; -1
 // elsewhere.
@@ -786,6 +792,156 @@ __device__ __forceinline__ int run_hit(const double (&w)[SP_PER], double start, 
     return at;
 }
 
+// The cluster's gathered candidates into the leader's lst, in index order.
+__device__ void pull_list(SampleSmem& sm, const uint32_t* ccnt, int n) {
+    for (int i = threadIdx.x; i < n; i += SP_THREADS) {
+        uint32_t j = i, c = 0;
+        while (j >= ccnt[c]) j -= ccnt[c++];
+        unsigned long long k;
+        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(sp_mapa(&sm.loc[j], c)) : "memory");
+        sm.lst[i] = k;
+    }
+}
+
+// The border token of a list in index order: the k-th of the descending order
+// (k > 0), or the first at which A plus the running weight reaches the target
+// (entries under `least` weigh nothing).  Returns its composite key, with a
+// zero index part where no tie of it stays behind; `dropped` counts the ties
+// that do.  srt is scratch for n keys.  All threads of the leader call it.
+__device__ unsigned long long border_of(SampleSmem& sm, const unsigned long long* lst, unsigned long long* srt, int n,
+                                        int ksh, const SpScale& sc, unsigned long long least, uint32_t k, double A,
+                                        double target, uint32_t& dropped) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (n + SP_THREADS - 1) / SP_THREADS;
+    const int nwarps = min(SP_WARPS, (n + 32 * per - 1) / (32 * per));
+    const double want = target - A;
+    if (n > 128) {
+        // few distinct logits (bf16): count each, and take the border's ties in index order
+        uint32_t kmin = 0xffffffffu, kmax = 0;
+        for (int i = tid; i < n; i += SP_THREADS) {
+            const uint32_t x = static_cast<uint32_t>(lst[i] >> 32) >> ksh;
+            kmin = min(kmin, x);
+            kmax = max(kmax, x);
+        }
+        kmin = __reduce_min_sync(0xffffffffu, kmin);
+        kmax = __reduce_max_sync(0xffffffffu, kmax);
+        __syncthreads();
+        if (lane == 0) {
+            sm.wcnt[warp] = kmin;
+            sm.scan[warp] = kmax;
+        }
+        for (int i = tid; i < SP_BINS; i += SP_THREADS) sm.cnt[i] = 0;
+        __syncthreads();
+        for (int w = 0; w < SP_WARPS; ++w) {
+            kmin = min(kmin, sm.wcnt[w]);
+            kmax = max(kmax, static_cast<uint32_t>(sm.scan[w]));
+        }
+        if (kmax - kmin < SP_BINS) {
+            for (int i = tid; i < n; i += SP_THREADS) atomicAdd(&sm.cnt[kmax - (static_cast<uint32_t>(lst[i] >> 32) >> ksh)], 1u);
+            if (tid == 0) {
+                sm.nb0 = kmax - kmin;
+                sm.keep = n;
+            }
+            __syncthreads();
+            uint32_t c[SP_BPT];
+            double m[SP_BPT], own = 0.0, start, end, total;
+#pragma unroll
+            for (int j = 0; j < SP_BPT; ++j) {
+                const uint32_t b = SP_BPT * tid + j;
+                c[j] = sm.cnt[b];
+                m[j] = c[j];
+                if (k == 0 && c[j]) {
+                    const uint32_t okey = ((kmax - b) << ksh) | (ksh && !((kmax - b) >> 15) ? 0xffffu : 0u);
+                    m[j] = (static_cast<unsigned long long>(okey) << 32 | 0xffffffffu) >= least ? c[j] * sc.weight(key_value(okey)) : 0.0;
+                }
+                own += m[j];
+            }
+            block_runs(sm, own, SP_WARPS, start, end, total);
+            const double goal = k > 0 ? static_cast<double>(min(k, static_cast<uint32_t>(n))) : want > 0.0 ? want : 0x1p-64;
+            if (start < goal && end >= goal) {
+                int at = -1;
+                double acc = start, before = start;
+#pragma unroll
+                for (int j = 0; j < SP_BPT; ++j) {
+                    if (c[j] && m[j] > 0.0 && (at < 0 || acc < goal)) {
+                        at = j;
+                        before = acc;
+                    }
+                    acc += m[j];
+                }
+                if (at >= 0) {
+#pragma unroll
+                    for (int j = 0; j < SP_BPT; ++j)
+                        if (j == at) {
+                            const double need = ceil((goal - before) / (m[j] / c[j]));
+                            sm.nb0 = SP_BPT * tid + j;
+                            sm.keep = need < 1.0 ? 1u : need > c[j] ? c[j] : static_cast<uint32_t>(need);
+                        }
+                }
+            }
+            __syncthreads();
+            // the keep-th entry of that logit
+            const uint32_t key = kmax - sm.nb0, ties = sm.cnt[sm.nb0], keep = min(sm.keep, ties);
+            uint32_t mine = 0;
+            for (int e = 0; e < per; ++e) {
+                const int i = tid * per + e;
+                mine += i < n && (static_cast<uint32_t>(lst[i] >> 32) >> ksh) == key ? 1u : 0u;
+            }
+            const uint32_t inc = warp_scan(mine, lane);
+            if (lane == 31) sm.wcnt[warp] = inc;
+            __syncthreads();
+            uint32_t ex = inc - mine;
+            for (int w = 0; w < warp; ++w) ex += sm.wcnt[w];
+            for (int e = 0; e < per; ++e) {
+                const int i = tid * per + e;
+                if (i < n && (static_cast<uint32_t>(lst[i] >> 32) >> ksh) == key && ++ex == keep) sm.sel_key = lst[i];
+            }
+            __syncthreads();
+            dropped = ties - keep;
+            const unsigned long long cut = sm.sel_key;
+            __syncthreads();
+            return dropped ? cut : cut & 0xffffffff00000000ull;
+        }
+    }
+    __syncthreads();
+    sort_list(sm, lst, srt, n);
+    if (tid == 0) {
+        sm.keep = k > 0 ? min(k, static_cast<uint32_t>(n)) : want > 0.0 ? n : 1;
+        sm.dropped = 0;
+    }
+    if (k == 0) {
+        double w[SP_PER], own = 0.0, start, end, total;
+#pragma unroll
+        for (int e = 0; e < SP_PER; ++e) {
+            const int j = tid * per + e;
+            w[e] = e < per && j < n && srt[j] >= least ? sc.weight(composite_value(srt[j])) : 0.0;
+            own += w[e];
+        }
+        block_runs(sm, own, nwarps, start, end, total);
+        // the first token at which the running sum reaches the target
+        if (start < want && end >= want) {
+            double acc = start;
+            int at = -1;
+#pragma unroll
+            for (int e = 0; e < SP_PER; ++e) {
+                if (w[e] > 0.0 && (at < 0 || acc < want)) at = e;
+                acc += w[e];
+            }
+            sm.keep = tid * per + at + 1;
+        }
+    }
+    __syncthreads();
+    const int at = max(0, static_cast<int>(sm.keep) - 1);
+    const unsigned long long cut = srt[at];
+    uint32_t drop = 0;
+    for (int j = tid; j < n; j += SP_THREADS) drop += j > at && srt[j] >> 32 == cut >> 32 ? 1u : 0u;
+    if (drop) atomicAdd(&sm.dropped, drop);
+    __syncthreads();
+    dropped = sm.dropped;
+    __syncthreads();
+    return dropped ? cut : cut & 0xffffffff00000000ull;
+}
+
 struct SpRow {
     bool by_k, by_p;
     int k;
@@ -797,18 +953,22 @@ struct SpRow {
 };
 
 // The leader's end of a row whose kept tokens all lie in the list lst[0..n):
-// filters, acceptance of the draft, the draw.  S_all: the row's sum before
-// top-p, or negative where the list is the whole row.
+// filters, acceptance of the draft, the draw.  Entries under lcut carry no
+// weight.  S_all: the row's sum before top-p, or negative where the list has
+// all of the row's weight.
 template <bool VERIFY>
-__device__ void draw_from_list(SampleSmem& sm, int n, const SpScale& sc, const SpRow& r, double S_all, int32_t* token) {
+__device__ void draw_from_list(SampleSmem& sm, int n, int ksh, float lcut, const SpScale& sc, const SpRow& r, double S_all,
+                               int32_t* token) {
     const int tid = threadIdx.x;
-    const unsigned long long* lst = sm.l.lst;
-    unsigned long long* srt = sm.l.loc;
+    if (n <= 0) return;   // (the list holds the maximum)
+    const unsigned long long* lst = sm.lst;
+    unsigned long long* srt = sm.loc;
     const int per = (n + SP_THREADS - 1) / SP_THREADS;
     const int nwarps = min(SP_WARPS, (n + 32 * per - 1) / (32 * per));
-    int nk = r.by_k ? min(r.k, n) : n;
-    unsigned long long cut = 0;
-    if (nk < n || r.by_p) {
+    const unsigned long long least = static_cast<unsigned long long>(order_key(lcut)) << 32;
+    unsigned long long cut = least;
+    if (n <= 128 && (r.by_k || r.by_p)) {   // one short sort serves both filters
+        int nk = r.by_k ? min(r.k, n) : n;
         sort_list(sm, lst, srt, n);
         if (r.by_p) {
             if (tid == 0) sm.keep = nk;
@@ -816,7 +976,7 @@ __device__ void draw_from_list(SampleSmem& sm, int n, const SpScale& sc, const S
 #pragma unroll
             for (int e = 0; e < SP_PER; ++e) {
                 const int j = tid * per + e;
-                w[e] = e < per && j < nk ? sc.weight(composite_value(srt[j])) : 0.0;
+                w[e] = e < per && j < nk && srt[j] >= least ? sc.weight(composite_value(srt[j])) : 0.0;
                 own += w[e];
             }
             block_runs(sm, own, nwarps, start, end, total);
@@ -835,7 +995,23 @@ __device__ void draw_from_list(SampleSmem& sm, int n, const SpScale& sc, const S
             __syncthreads();
             nk = sm.keep;
         }
-        cut = srt[nk - 1];
+        cut = max(least, srt[nk - 1]);
+    } else if (r.by_k || r.by_p) {
+        uint32_t drop;
+        if (r.by_k) cut = max(least, border_of(sm, lst, srt, n, ksh, sc, least, static_cast<uint32_t>(r.k), 0.0, 0.0, drop));
+        if (r.by_p) {
+            double S = S_all;
+            if (r.by_k || S_all < 0.0) {
+                double own = 0.0, start, end;
+                for (int e = 0; e < per; ++e) {
+                    const int j = tid * per + e;
+                    if (j < n && lst[j] >= cut) own += sc.weight(composite_value(lst[j]));
+                }
+                block_runs(sm, own, nwarps, start, end, S);
+            }
+            // tokens that top-k left out come behind the border in the order
+            cut = max(cut, border_of(sm, lst, srt, n, ksh, sc, least, 0, 0.0, fmax(r.p * S, 1e-9), drop));
+        }
     }
     if (tid == 0) sm.wx = 0.0;
     __syncthreads();
@@ -906,9 +1082,7 @@ __device__ void segment_sums(double* sums, const SpChunk<TL>& ck, uint32_t rank,
     double s0 = 0.0, s1 = 0.0;
     const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(tau);
     for (int v0 = q0; v0 < q1; v0 += 32) add_weights<TL>(ck.raw_to(v0 + lane, q1), tau, tb, sc, s0, s1);
-    const double s = warp_sum_f64(s0 + s1);
-    if (lane < static_cast<int>(C)) st_cluster_f64(&sums[rank * SP_WARPS + warp], lane, s);
-    cluster_sync_all();
+    share_sums(sums, s0 + s1, rank, C);
 }
 
 // One element of the residual max(w - q S, 0) of the weights at or above tau
@@ -934,9 +1108,7 @@ __device__ void residual_sums(double* sums, const SpChunk<TL>& ck, uint32_t rank
 #pragma unroll
         for (int e = 0; e < VEC; ++e) s += left_weight<TL>(v[e], ck.index(v0, e), tau, sc, q, S);
     }
-    s = warp_sum_f64(s);
-    if (lane < static_cast<int>(C)) st_cluster_f64(&sums[rank * SP_WARPS + warp], lane, s);
-    cluster_sync_all();
+    share_sums(sums, s, rank, C);
 }
 
 // The first index whose cumulative weight exceeds u times the total.  Returns
@@ -1019,21 +1191,197 @@ __device__ int draw_token(const double* sums, const SpChunk<TL>& ck, uint32_t ra
     return last;
 }
 
-// Index of the keep-th token with logit tau, in index order, of `ties` in the
-// row (two cluster barriers).
+// The elements of the border's intervals b0..b1: listed in every CTA's loc, or,
+// where one CTA has too many, found by passes over the row.
+struct SpWindow {
+    bool listed;
+    uint32_t mine, start, count;   // this CTA's entries; this warp's range of them
+    float bot, top;                // bounds of the intervals' logits
+    SpBins bins;
+    uint32_t b0, b1;
+};
+template <typename TL, typename F>
+__device__ __forceinline__ void each_in(const SampleSmem& sm, const SpChunk<TL>& ck, const SpWindow& w, F f) {
+    if (w.listed) {
+        for (uint32_t i = threadIdx.x; i < w.mine; i += SP_THREADS) f(composite_value(sm.loc[i]));
+        return;
+    }
+    constexpr int VEC = SpElem<TL>::VEC;
+    const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(w.bot);
+    for (int q = threadIdx.x; q < ck.nvec; q += SP_THREADS) {
+        const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[q];
+        if (!SpElem<TL>::any_ge(raw, tb)) continue;
+        float v[VEC];
+        SpElem<TL>::unpack(raw, v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            if (!(v[e] >= w.bot && v[e] <= w.top)) continue;
+            const uint32_t b = w.bins.of(v[e]);
+            if (b >= w.b0 && b <= w.b1) f(v[e]);
+        }
+    }
+}
 template <typename TL>
-__device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float tau, uint32_t keep) {
+__device__ SpWindow make_window(SampleSmem& sm, uint32_t* ccnt, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float lo,
+                                const SpBins& bins, uint32_t b0, uint32_t b1) {
+    SpWindow w;
+    w.bins = bins;
+    w.b0 = b0;
+    w.b1 = b1;
+    w.bot = bins.lower(b1, lo);
+    w.top = bins.upper(b0);
+    gather<TL>(sm, ccnt, ck, rank, C, w.bot, [&](float l) { const uint32_t b = bins.of(l); return b >= b0 && b <= b1; },
+               &w.start, &w.count);
+    uint32_t most = 0;
+    for (uint32_t r = 0; r < C; ++r) most = max(most, ccnt[r]);
+    w.listed = most <= SP_CAP;
+    w.mine = ccnt[rank];
+    return w;
+}
+
+// The border key of a window: with k > 0 the key at which the count A of the
+// tokens above the window plus the running count reaches k, else the one at
+// which the weight A above it plus the running weight reaches the target.
+// SP_BINS key ranges at a time: counts times the weights of a range's ends
+// bound its running sums, so that exact sums are needed of one range only; a
+// range of a single key is exact.  keep: how many of the `ties` tokens of that
+// key are on this side of the border.  All threads of the cluster call it.
+template <typename TL>
+__device__ uint32_t refine(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
+                           const SpWindow& w, bool by_count, double A, double target, uint32_t& keep, uint32_t& ties) {
+    constexpr int KSH = SpElem<TL>::KSH;
+    const int tid = threadIdx.x, lane = tid & 31;
+    uint32_t khi = order_key(w.top) >> KSH, klo = order_key(w.bot) >> KSH;
+    while (true) {
+        int sh = 0;
+        while (((khi - klo) >> sh) >= SP_BINS) ++sh;
+        const uint32_t span = (1u << sh) - 1;
+        for (int i = tid; i < SP_BINS; i += SP_THREADS) sm.cnt[i] = 0;
+        if (tid == 0) {
+            sm.nb0 = SP_BINS;
+            sm.nb1 = SP_BINS;
+            sm.last = 0;
+        }
+        __syncthreads();
+        each_in<TL>(sm, ck, w, [&](float l) {
+            const uint32_t key = order_key(l) >> KSH;
+            if (key >= klo && key <= khi) atomicAdd(&sm.cnt[(khi - key) >> sh], 1u);
+        });
+        cluster_sync_warp0();
+        uint32_t n[SP_BPT];
+        pull_counts(sm, C, n);
+        double hi[SP_BPT], low[SP_BPT], hown = 0.0, lown = 0.0, hs, he, ls, le, total;
+#pragma unroll
+        for (int j = 0; j < SP_BPT; ++j) {
+            const uint32_t b = SP_BPT * tid + j;
+            hi[j] = low[j] = n[j];
+            if (!by_count && n[j]) {
+                const uint32_t top = khi - (b << sh), bot = top - klo > span ? top - span : klo;
+                hi[j] *= sc.weight(key_logit<TL>(top));
+                low[j] = sh ? low[j] * sc.weight(key_logit<TL>(bot)) : hi[j];
+            }
+            hown += hi[j];
+            lown += low[j];
+            if (n[j]) atomicMax(&sm.last, static_cast<int>(b));
+        }
+        block_runs(sm, hown, SP_WARPS, hs, he, total);
+        block_runs(sm, lown, SP_WARPS, ls, le, total);
+        hs += A;
+        ls += A;
+        const double from = ls;   // the running sum at this thread's first bin
+        uint32_t f0 = SP_BINS, f1 = SP_BINS;
+#pragma unroll
+        for (int j = 0; j < SP_BPT; ++j) {
+            hs += hi[j];
+            ls += low[j];
+            if (hs * (1.0 + 1e-12) >= target) f0 = min(f0, static_cast<uint32_t>(SP_BPT * tid + j));
+            if (ls >= target) f1 = min(f1, static_cast<uint32_t>(SP_BPT * tid + j));
+        }
+        f0 = __reduce_min_sync(0xffffffffu, f0);
+        f1 = __reduce_min_sync(0xffffffffu, f1);
+        if (lane == 0) {
+            atomicMin(&sm.nb0, f0);
+            atomicMin(&sm.nb1, f1);
+        }
+        __syncthreads();
+        const uint32_t b1 = min(sm.nb1, static_cast<uint32_t>(sm.last));
+        const uint32_t b0 = sh == 0 || by_count ? b1 : min(sm.nb0, b1);
+        if (sh == 0 || by_count) {
+            ls = from;
+#pragma unroll
+            for (int j = 0; j < SP_BPT; ++j) {
+                if (b1 == static_cast<uint32_t>(SP_BPT * tid + j)) {
+                    sm.sel_before = ls;
+                    sm.sel_cnt = n[j];
+                    sm.sel_w = n[j] ? low[j] / n[j] : 1.0;
+                }
+                ls += low[j];
+            }
+            __syncthreads();
+            if (sh == 0) {
+                ties = sm.sel_cnt;
+                const double need = ceil((target - sm.sel_before) / sm.sel_w);
+                keep = need < 1.0 ? 1u : need >= static_cast<double>(ties) ? ties : static_cast<uint32_t>(need);
+                return khi - b1;
+            }
+            A = sm.sel_before;
+            khi -= b1 << sh;
+            klo = khi - klo > span ? khi - span : klo;
+            cluster_sync_warp0();   // the counts have been read
+            continue;
+        }
+        // the sums before range b0, and of it
+        const uint32_t top = khi - (b0 << sh), bot = top - klo > span ? top - span : klo;
+        double before = 0.0, of = 0.0;
+        each_in<TL>(sm, ck, w, [&](float l) {
+            const uint32_t key = order_key(l) >> KSH;
+            if (key < bot || key > khi) return;
+            const double x = sc.weight(l);
+            if (key > top) before += x;
+            else of += x;
+        });
+        share_sums(sm.rsum, before, rank, C);
+        before = table_sum(sm.rsum, C, lane);
+        share_sums(sm.wsum, of, rank, C);
+        of = table_sum(sm.wsum, C, lane);
+        A += before;
+        if (A + of >= target || bot == klo || b0 == b1) {
+            khi = top;
+            klo = bot;
+        } else {
+            A += of;
+            const uint32_t end = khi - (b1 << sh);
+            khi = bot - 1;
+            klo = end - klo > span ? end - span : klo;
+        }
+        cluster_sync_warp0();   // the tables have been read
+    }
+}
+
+// Index of the keep-th token with logit tau, in index order (two cluster
+// barriers).
+template <typename TL>
+__device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, const SpWindow& win, float tau,
+                         uint32_t keep) {
     constexpr int VEC = SpElem<TL>::VEC;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
-    uint32_t n = 0;
-    for (int q = q0 + lane; q < q1; q += 32) {
+    // this warp's ties, in index order along lanes and steps of 32 entries or vectors
+    const int first = win.listed ? static_cast<int>(win.start) : q0;
+    const int last = win.listed ? static_cast<int>(win.start + win.count) : q1;
+    auto ties_at = [&](int i) -> uint32_t {   // a bit per element of entry or vector i
+        if (i >= last) return 0;
+        if (win.listed) return composite_value(sm.loc[i]) == tau ? 1u : 0u;
         float v[VEC];
-        ck.load(q, v);
+        ck.load(i, v);
+        uint32_t mask = 0;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) n += v[e] == tau ? 1u : 0u;
-    }
+        for (int e = 0; e < VEC; ++e) mask |= (v[e] == tau ? 1u : 0u) << e;
+        return mask;
+    };
+    uint32_t n = 0;
+    for (int i = first + lane; i < last; i += 32) n += __popc(ties_at(i));
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) sm.wcnt[warp] = n;
     __syncthreads();
@@ -1043,24 +1391,19 @@ __device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, u
         tot += sm.wcnt[w];
     }
     if (tid < static_cast<int>(C)) st_cluster_s32(&sm.tie[rank], tid, static_cast<int>(tot));
-    cluster_sync_all();
+    cluster_sync_warp0();
     for (uint32_t r = 0; r < rank; ++r) before += sm.tie[r];
     if (keep > before && keep <= before + n) {
         uint32_t left = keep - before;   // 1-based
-        for (int v0 = q0; v0 < q1; v0 += 32) {
-            uint32_t mask = 0;
-            if (v0 + lane < q1) {
-                float v[VEC];
-                ck.load(v0 + lane, v);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) mask |= (v[e] == tau ? 1u : 0u) << e;
-            }
+        for (int i0 = first; i0 < last; i0 += 32) {
+            uint32_t mask = ties_at(i0 + lane);
             const uint32_t mine = __popc(mask);
             const uint32_t in = warp_scan(mine, lane);
             if (in >= left && in - mine < left) {
                 uint32_t skip = left - (in - mine) - 1;
                 while (skip--) mask &= mask - 1;
-                for (uint32_t r = 0; r < C; ++r) st_cluster_s32(&sm.cut_idx, r, ck.index(v0 + lane, __ffs(mask) - 1));
+                const int idx = win.listed ? composite_index(sm.loc[i0 + lane]) : ck.index(i0 + lane, __ffs(mask) - 1);
+                for (uint32_t r = 0; r < C; ++r) st_cluster_s32(&sm.cut_idx, r, idx);
             }
             const uint32_t t = __shfl_sync(0xffffffffu, in, 31);
             if (t >= left) break;
@@ -1071,6 +1414,12 @@ __device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, u
     return static_cast<int>(sm.cut_idx);
 }
 
+// The count table of every CTA to zero (one cluster barrier).
+__device__ void clear_counts(SampleSmem& sm) {
+    for (int i = threadIdx.x; i < SP_BINS + 31; i += SP_THREADS) sm.cnt[i] = 0;
+    cluster_sync_warp0();
+}
+
 // Masks this CTA's elements equal to tau behind index icut.
 template <typename TL>
 __device__ void mask_ties(const SpChunk<TL>& ck, float tau, int icut) {
@@ -1078,11 +1427,9 @@ __device__ void mask_ties(const SpChunk<TL>& ck, float tau, int icut) {
         if (static_cast<float>(ck.buf[ck.mis + i]) == tau) ck.buf[ck.mis + i] = SpElem<TL>::ninf();
 }
 
-// Sum of the weights at or above lo in intervals before b0, the same in every
-// thread (one cluster barrier).
+// This thread's sum of the weights at or above lo in intervals before b0.
 template <typename TL>
-__device__ double above_sum(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float lo,
-                            const SpBins& bins, uint32_t b0, const SpScale& sc) {
+__device__ double above_part(const SpChunk<TL>& ck, float lo, const SpBins& bins, uint32_t b0, const SpScale& sc) {
     constexpr int VEC = SpElem<TL>::VEC;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int q0, q1;
@@ -1105,10 +1452,42 @@ __device__ double above_sum(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank
             }
         }
     }
-    s = warp_sum_f64(s);
-    if (lane < static_cast<int>(C)) st_cluster_f64(&sm.rsum[rank * SP_WARPS + warp], lane, s);
-    cluster_sync_all();
-    return table_sum(sm.rsum, C, lane);
+    return s;
+}
+
+// The same for the window's weights that are kept, after masking those of its
+// ties at tau that are not.
+template <typename TL>
+__device__ double border_part(const SampleSmem& sm, const SpChunk<TL>& ck, const SpWindow& win, unsigned long long cut,
+                              const SpScale& sc) {
+    constexpr int VEC = SpElem<TL>::VEC;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float tau = composite_value(cut);
+    if (win.listed) {
+        double s = 0.0;
+        for (uint32_t i = win.start + lane; i < win.start + win.count; i += 32) {
+            const unsigned long long k = sm.loc[i];
+            if (k >= cut) s += sc.weight(composite_value(k));
+            else if (k >> 32 == cut >> 32) ck.mask(composite_index(k));
+        }
+        return s;
+    }
+    if (static_cast<uint32_t>(cut) != 0) mask_ties<TL>(ck, tau, composite_index(cut));
+    __syncthreads();
+    const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(tau);
+    int q0, q1;
+    warp_segment(ck.nvec, warp, q0, q1);
+    double s = 0.0;
+    for (int v0 = q0; v0 < q1; v0 += 32) {
+        const uint4 raw = ck.raw_to(v0 + lane, q1);
+        if (!__any_sync(0xffffffffu, SpElem<TL>::any_ge(raw, tb))) continue;
+        float v[VEC];
+        SpElem<TL>::unpack(raw, v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (v[e] >= tau && v[e] <= win.top && win.bins.of(v[e]) >= win.b0) s += sc.weight(v[e]);
+    }
+    return s;
 }
 
 // The row's part of probs: w / S in fp32, 0 below tau.
@@ -1159,9 +1538,38 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
     const int row = blockIdx.x / a.cluster;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < 16) sm.tab[tid] = __hiloint2double(__double2hiint(exp2(tid / 16.0)) - (tid << 16), __double2loint(exp2(tid / 16.0)));
-    for (int i = tid; i < SP_BINS; i += SP_THREADS) sm.cnt[i] = 0;
+    for (int i = tid; i < SP_BINS + 31; i += SP_THREADS) sm.cnt[i] = 0;
+    cluster_arrive();   // waited for before the first store to another CTA: all have started then
     grid_dep_wait();
     grid_dep_launch();
+
+    // ---- the row's parameters
+    const int seq = VERIFY ? row / a.per : row, pj = VERIFY ? row % a.per : 0;
+    double T = a.temperature ? static_cast<double>(__ldg(a.temperature + seq)) : 1.0;
+    SpRow r;
+    r.k = a.top_k ? __ldg(a.top_k + seq) : 0;
+    r.p = a.top_p ? static_cast<double>(__ldg(a.top_p + seq)) : 2.0;
+    double mp = a.min_p ? static_cast<double>(__ldg(a.min_p + seq)) : 0.0;
+    if (!(T > 0.0)) {   // greedy
+        T = 1.0;
+        r.k = 1;
+        r.p = 2.0;
+        mp = 0.0;
+    }
+    r.by_k = r.k > 0 && r.k < a.V;
+    r.by_p = r.p < 1.0;
+    r.has_draft = VERIFY && pj < a.per - 1;
+    r.x = -1;
+    r.q = nullptr;
+    r.ua = 0.0;
+    if (r.has_draft) {
+        r.x = __ldg(a.draft + static_cast<size_t>(seq) * (a.per - 1) + pj);
+        if (r.x < 0 || r.x >= a.V) r.x = -1;
+        if (a.q) r.q = a.q + (static_cast<size_t>(seq) * (a.per - 1) + pj) * a.V;
+        r.ua = static_cast<double>(__ldg(a.u + static_cast<size_t>(seq) * a.per + pj));
+    }
+    r.us = static_cast<double>(__ldg(a.u + (VERIFY ? static_cast<size_t>(seq) * a.per + a.per - 1 : static_cast<size_t>(row))));
+    r.us = fmin(r.us, 1.0 - 0x1p-24);
 
     // ---- the row's part into shared memory, and its maximum
     SpChunk<TL> ck;
@@ -1197,51 +1605,35 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
         }
     }
     const float mine = tmax.get();
-    float m = mine;
+    float m = mine, low = mine > -INFINITY ? mine : INFINITY;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) sm.wmax[warp] = m;
+    for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+    }
+    if (lane == 0) {
+        sm.wmax[warp] = m;
+        sm.wmin[warp] = low;
+    }
     __syncthreads();
-    if (warp == 0) {
-        m = lane < SP_WARPS ? sm.wmax[lane] : -INFINITY;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane < static_cast<int>(C)) st_cluster_f32(&sm.cmax[rank], lane, m);
+    for (int w = 0; w < SP_WARPS; ++w) {
+        m = fmaxf(m, sm.wmax[w]);
+        low = fminf(low, sm.wmin[w]);
     }
-
-    // ---- the row's parameters
-    const int seq = row / a.per, pj = row % a.per;
-    double T = a.temperature ? static_cast<double>(__ldg(a.temperature + seq)) : 1.0;
-    SpRow r;
-    r.k = a.top_k ? __ldg(a.top_k + seq) : 0;
-    r.p = a.top_p ? static_cast<double>(__ldg(a.top_p + seq)) : 2.0;
-    double mp = a.min_p ? static_cast<double>(__ldg(a.min_p + seq)) : 0.0;
-    if (!(T > 0.0)) {   // greedy
-        T = 1.0;
-        r.k = 1;
-        r.p = 2.0;
-        mp = 0.0;
+    cluster_wait();
+    if (tid < static_cast<int>(C)) {
+        st_cluster_f32(&sm.cmax[rank], tid, m);
+        st_cluster_f32(&sm.cmin[rank], tid, low);
     }
-    r.by_k = r.k > 0 && r.k < a.V;
-    r.by_p = r.p < 1.0;
-    r.has_draft = VERIFY && pj < a.per - 1;
-    r.x = -1;
-    r.q = nullptr;
-    r.ua = 0.0;
-    if (r.has_draft) {
-        r.x = __ldg(a.draft + static_cast<size_t>(seq) * (a.per - 1) + pj);
-        if (r.x < 0 || r.x >= a.V) r.x = -1;
-        if (a.q) r.q = a.q + (static_cast<size_t>(seq) * (a.per - 1) + pj) * a.V;
-        r.ua = static_cast<double>(__ldg(a.u + static_cast<size_t>(seq) * a.per + pj));
-    }
-    r.us = static_cast<double>(__ldg(a.u + (VERIFY ? static_cast<size_t>(seq) * a.per + a.per - 1 : static_cast<size_t>(row))));
-    r.us = fmin(r.us, 1.0 - 0x1p-24);
-
-    T = fmax(T, 1e-30);
-
-    cluster_sync_all();
+    cluster_sync_warp0();
     m = -INFINITY;
-    for (uint32_t i = 0; i < C; ++i) m = fmaxf(m, sm.cmax[i]);
+    low = INFINITY;
+    for (uint32_t i = 0; i < C; ++i) {
+        m = fmaxf(m, sm.cmax[i]);
+        low = fminf(low, sm.cmin[i]);
+    }
+    T = fmax(T, 1e-30);
     const double c = 1.4426950408889634 / T;
     const SpScale sc{m, scaled_f64(m), c * 0x1p896, c, sm.tab};
     double dmin = -44.361419555836498 * T;   // 64 ln 2
@@ -1257,12 +1649,12 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
 
     // ---- few candidates: a list of them, finished by the leader
     uint32_t n = 0xffffffffu;
+    uint32_t* ccnt = sm.ccnt[0];
     double S_all = -1.0;
-    float list_lo = lcut;
-    if (mp > 0.0) n = gather<TL>(sm, ck, rank, C, lcut, [](float) { return true; });
+    if (mp > 0.0) n = gather<TL>(sm, ccnt = sm.ccnt[0], ck, rank, C, lcut, [](float) { return true; });
     if (n > SP_CAP && r.by_k && r.k <= SP_CAP) {
-        list_lo = kth_bound(sm, sc, C, lcut, mine, static_cast<uint32_t>(r.k));
-        n = gather<TL>(sm, ck, rank, C, list_lo, [](float) { return true; });
+        const float lo = kth_bound(sm, C, lcut, low, m, mine, static_cast<uint32_t>(r.k));
+        n = gather<TL>(sm, ccnt = sm.ccnt[1], ck, rank, C, lo, [](float) { return true; });
     }
     SpNucleus nu{};
     if (n > SP_CAP && r.by_p && !r.by_k) {
@@ -1270,22 +1662,16 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
         S_all = nu.S;
         if (nu.n <= SP_CAP) {
             const SpBins bins = first_bins(sc, lcut);
-            n = gather<TL>(sm, ck, rank, C, bins.lower(nu.b1, lcut), [&](float l) { return bins.of(l) <= nu.b1; });
+            n = gather<TL>(sm, ccnt = sm.ccnt[1], ck, rank, C, bins.lower(nu.b1, lcut), [&](float l) { return bins.of(l) <= nu.b1; });
         }
     }
     if (n <= SP_CAP) {
         if (rank == 0) {
-            for (int i = tid; i < static_cast<int>(n); i += SP_THREADS) {
-                uint32_t j = i, c = 0;
-                while (j >= sm.ccnt[c]) j -= sm.ccnt[c++];
-                unsigned long long k;
-                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(sp_mapa(&sm.l.loc[j], c)) : "memory");
-                sm.l.lst[i] = k;
-            }
+            pull_list(sm, ccnt, static_cast<int>(n));
         }
-        cluster_sync_all();   // the other CTAs' lists have been read
+        cluster_sync_warp0();   // the other CTAs' lists have been read
         if (rank == 0)
-            draw_from_list<VERIFY>(sm, static_cast<int>(n), sc, r, S_all, a.token + row);
+            draw_from_list<VERIFY>(sm, static_cast<int>(n), SpElem<TL>::KSH, lcut, sc, r, S_all, a.token + row);
         if (VERIFY || !a.probs) return;
         if (rank == 0) {
             __syncthreads();
@@ -1294,7 +1680,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
                 st_cluster_f64(&sm.list_sum, tid, sm.list_sum);
             }
         }
-        cluster_sync_all();
+        cluster_sync_warp0();
     }
 
     // ---- many: the border of the kept set by selection over the whole row, then sums and the draw
@@ -1302,62 +1688,81 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
     double S = 0.0;
     if (n <= SP_CAP) {
         S = sm.list_sum;
-        tau = list_lo;             // the whole list is kept where it has no cut
-        if (sm.list_cut) {
-            tau = composite_value(sm.list_cut);
+        tau = composite_value(sm.list_cut);
+        if (static_cast<uint32_t>(sm.list_cut) != 0) {   // else all ties are kept
             mask_ties<TL>(ck, tau, composite_index(sm.list_cut));
             __syncthreads();
         }
     } else {
+        bool summed = false;           // wsum holds the kept weights' sums
         if (r.by_k || r.by_p) {
-            SpBin at{};
-            unsigned long long keep = 0;   // how many of the tokens at the border are kept
+            unsigned long long cut = 0;
+            uint32_t dropped = 0;   // ties of the k-th token that top-k leaves behind
             if (r.by_k) {
-                tau = key_logit<TL>(select_kth<TL>(sm, ck, sc, rank, C, lcut, r.k, at));
-                const unsigned long long k = static_cast<unsigned long long>(r.k);
-                keep = min(k - min(at.above, k), static_cast<unsigned long long>(at.cnt));
+                clear_counts(sm);
+                const SpKth kt = kth_interval<TL>(sm, ck, sc, C, lcut, static_cast<uint32_t>(r.k));
+                const SpBins bins = first_bins(sc, lcut);
+                const uint32_t left = min(static_cast<uint32_t>(r.k) - min(kt.above, static_cast<uint32_t>(r.k) - 1), kt.cnt);
+                const SpWindow win = make_window<TL>(sm, sm.ccnt[2], ck, rank, C, lcut, bins, kt.b, kt.b);
+                uint32_t keep, ties;
+                const float v = key_logit<TL>(refine<TL>(sm, ck, sc, rank, C, win, true, static_cast<double>(kt.above),
+                                                         static_cast<double>(kt.above) + static_cast<double>(left), keep, ties));
+                dropped = ties - keep;
+                cut = composite(v, dropped ? tie_index<TL>(sm, ck, rank, C, win, v, keep) : -1);
             }
             if (r.by_p) {
-                const float kth = tau;
-                const unsigned long long kkeep = keep;
+                const float kth = r.by_k ? composite_value(cut) : lcut;
                 if (r.by_k) {
-                    for (int i = tid; i < SP_BINS; i += SP_THREADS) sm.cnt[i] = 0;
-                    cluster_sync_all();
-                    nu = nucleus<TL>(sm, ck, sc, rank, C, kth, r.p,
-                                     static_cast<double>(at.cnt - keep) * sc.weight(kth));
+                    clear_counts(sm);
+                    nu = nucleus<TL>(sm, ck, sc, rank, C, kth, r.p, static_cast<double>(dropped) * sc.weight(kth));
                 }
-                // the border lies in intervals b0..b1: the sum above them exactly, then key by key
+                // the border lies in intervals b0..b1: the sum above them, then token by token
                 const double target = fmax(r.p * nu.S, 1e-9);
                 const SpBins bins = first_bins(sc, kth);
-                const double A = above_sum<TL>(sm, ck, rank, C, kth, bins, nu.b0, sc);
-                at.above = static_cast<unsigned long long>(__double2ll_rn(A * static_cast<double>(1ull << SP_FIX)));
-                tau = key_logit<TL>(select_key<TL, true>(sm, ck, sc, rank, C, kth, nu.b0, nu.b1,
-                                                         target * static_cast<double>(1ull << SP_FIX), at));
-                const double need = ceil((target - static_cast<double>(at.above) / static_cast<double>(1ull << SP_FIX)) /
-                                         sc.weight(tau));
-                keep = need < 1.0 ? 1 : need >= static_cast<double>(at.cnt) ? at.cnt : static_cast<unsigned long long>(need);
-                if (r.by_k && tau == kth) keep = min(keep, kkeep);
+                const double mine_above = above_part<TL>(ck, kth, bins, nu.b0, sc);
+                share_sums(sm.rsum, mine_above, rank, C);
+                const double A = table_sum(sm.rsum, C, lane);
+                const SpWindow win = make_window<TL>(sm, sm.ccnt[3], ck, rank, C, kth, bins, nu.b0, nu.b1);
+                uint32_t keep, ties;
+                const float v = key_logit<TL>(refine<TL>(sm, ck, sc, rank, C, win, false, A, target, keep, ties));
+                cut = max(cut, composite(v, keep < ties ? tie_index<TL>(sm, ck, rank, C, win, v, keep) : -1));
+                tau = composite_value(cut);
+                const double mine_border = border_part<TL>(sm, ck, win, cut, sc);
+                share_sums(sm.wsum, mine_above + mine_border, rank, C);
+                summed = true;
+            } else {
+                tau = composite_value(cut);
+                if (static_cast<uint32_t>(cut) != 0) mask_ties<TL>(ck, tau, composite_index(cut));
+                __syncthreads();
             }
-            if (keep < at.cnt) mask_ties<TL>(ck, tau, tie_index<TL>(sm, ck, rank, C, tau, static_cast<uint32_t>(keep)));
         }
         double wx = 0.0;
         if (r.x >= 0) {
-            __syncthreads();   // masked ties
-            // the draft's weight, where it is kept: from the one CTA that holds it
-            if (tid == 0) {
-                const int i = r.x - ck.begin;
-                if (i >= 0 && i < ck.n) {
-                    const float l = static_cast<float>(ck.buf[ck.mis + i]);
-                    const double w = l >= tau ? sc.weight(l) : 0.0;
-                    for (uint32_t j = 0; j < C; ++j) st_cluster_f64(&sm.wx, j, w);
-                    if (!r.q) ck.mask(r.x);   // a certain draft leaves the others
-                }
+            // the draft's weight, where it is kept, from the one CTA that holds it; a certain draft leaves the others
+            const int i = r.x - ck.begin;
+            if (i >= 0 && i < ck.n && tid == 0) {
+                const float l = static_cast<float>(ck.buf[ck.mis + i]);
+                const double w = l >= tau ? sc.weight(l) : 0.0;
+                for (uint32_t j = 0; j < C; ++j) st_cluster_f64(&sm.wx, j, w);
+                if (!r.q) ck.mask(r.x);
             }
+            if (summed) cluster_sync_warp0();
+            else __syncthreads();
         }
-        __syncthreads();
-        segment_sums<TL>(sm.wsum, ck, rank, C, tau, sc);
-        const double rest = table_sum(sm.wsum, C, lane);
+        if (!summed) segment_sums<TL>(sm.wsum, ck, rank, C, tau, sc);
         if (r.x >= 0) wx = sm.wx;
+        if (summed && wx > 0.0 && !r.q) {
+            // the draft's segment without it
+            const int c = r.x / a.chunk, first = c * a.chunk;
+            const TL* part = rowp + first;
+            const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(part) & 15u) / sizeof(TL));
+            const int vecs = (mis + min(a.chunk, a.V - first) + VEC - 1) / VEC, per = ((vecs + SP_WARPS - 1) / SP_WARPS + 31) & ~31;
+            const int seg = c * SP_WARPS + (mis + r.x - first) / VEC / per;
+            __syncthreads();
+            if (tid == 0) sm.wsum[seg] = fmax(0.0, sm.wsum[seg] - wx);
+            __syncthreads();
+        }
+        const double rest = table_sum(sm.wsum, C, lane);
         S = r.has_draft && !r.q ? rest + wx : rest;
         if (r.has_draft) {
             const double qx = r.q ? (r.x >= 0 ? static_cast<double>(__ldg(r.q + r.x)) : 0.0) : 1.0;
@@ -1424,8 +1829,12 @@ static ms_status sample_launch_t(const SampleArgs& a, cudaStream_t s) {
 }
 
 static ms_status sample_launch(SampleArgs a, ms_dtype dt, bool verify, cudaStream_t s) {
+    // The smallest cluster whose parts leave room for two CTAs per SM, then
+    // wider while all rows still run at once.
+    const int eb = dt == MS_BF16 ? 2 : 4;
     int C = 1;
-    while (C < SP_MAXC && a.V > 1024 * C) C *= 2;
+    while (C < SP_MAXC && static_cast<long>(a.V) * eb > 66L * 1024 * C) C *= 2;
+    while (C < SP_MAXC && a.V > 1024 * C && 2L * C * a.rows <= 2L * num_sms()) C *= 2;
     a.cluster = C;
     a.chunk = ((a.V + C - 1) / C + 7) / 8 * 8;
     if (dt == MS_BF16)
