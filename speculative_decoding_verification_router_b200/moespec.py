@@ -122,10 +122,6 @@ _LOGITS = {torch.float32: MS_F32, torch.bfloat16: MS_BF16}
 _SCORES = {"softmax": MS_SOFTMAX, "sigmoid": MS_SIGMOID}
 
 
-def _a(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
 def _rows(t: torch.Tensor, name: str, dims: int):
     """Checks a logits tensor; returns its shape."""
     if not t.is_cuda:
@@ -139,21 +135,21 @@ def _rows(t: torch.Tensor, name: str, dims: int):
     return t.shape
 
 
-def _vec(t: torch.Tensor, dtype, shape, name: str, dev):
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+def _vec(t: torch.Tensor, dtype, shape, name: str, dev) -> int:
+    """Checks a tensor's type, shape and device; returns its address."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def _filters(n: int, dev, temperature, top_k, top_p, min_p):
-    if temperature is not None:
-        _vec(temperature, torch.float32, (n,), "temperature", dev)
-    if top_k is not None:
-        _vec(top_k, torch.int32, (n,), "top_k", dev)
-    if top_p is not None:
-        _vec(top_p, torch.float32, (n,), "top_p", dev)
-    if min_p is not None:
-        _vec(min_p, torch.float32, (n,), "min_p", dev)
+    """Addresses of the sampling parameters, None where not given."""
+    shape = (n,)
+    return (None if temperature is None else _vec(temperature, torch.float32, shape, "temperature", dev),
+            None if top_k is None else _vec(top_k, torch.int32, shape, "top_k", dev),
+            None if top_p is None else _vec(top_p, torch.float32, shape, "top_p", dev),
+            None if min_p is None else _vec(min_p, torch.float32, shape, "min_p", dev))
 
 
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
@@ -286,18 +282,18 @@ def route_grouped(logits: torch.Tensor, k: int, score: str = "softmax", bias: Op
     if score not in _SCORES:
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
     dev = logits.device
-    if bias is not None:
-        _vec(bias, torch.float32, (E,), "bias", dev)
+    bias_p = None if bias is None else _vec(bias, torch.float32, (E,), "bias", dev)
     if out is None:
         idx = torch.empty(T, k, dtype=torch.int32, device=dev)
         w = torch.empty(T, k, dtype=torch.float32, device=dev)
+        idx_p, w_p = idx.data_ptr(), w.data_ptr()
     else:
         idx, w = out
-        _vec(idx, torch.int32, (T, k), "out[0]", dev)
-        _vec(w, torch.float32, (T, k), "out[1]", dev)
+        idx_p = _vec(idx, torch.int32, (T, k), "out[0]", dev)
+        w_p = _vec(w, torch.float32, (T, k), "out[1]", dev)
     _launch(_lib.moe_route_grouped, "moe_route_grouped", dev, stream, logits.data_ptr(), _LOGITS[logits.dtype],
-            _a(bias), T, E, _SCORES[score], n_groups, n_groups if topk_groups is None else topk_groups, group_top, k,
-            1 if renormalize else 0, scale, idx.data_ptr(), w.data_ptr())
+            bias_p, T, E, _SCORES[score], n_groups, n_groups if topk_groups is None else topk_groups, group_top, k,
+            1 if renormalize else 0, scale, idx_p, w_p)
     return idx, w
 
 
@@ -390,18 +386,22 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     Returns token [T] int32, or (token, probs [T, V] fp32) with return_probs."""
     T, V = _rows(logits, "logits", 2)
     dev = logits.device
-    _vec(u, torch.float32, (T,), "u", dev)
-    _filters(T, dev, temperature, top_k, top_p, min_p)
+    u_p = _vec(u, torch.float32, (T,), "u", dev)
+    filters = _filters(T, dev, temperature, top_k, top_p, min_p)
+    probs_p = None
     if out is None:
         token = torch.empty(T, dtype=torch.int32, device=dev)
-        probs = torch.empty((T, V), dtype=torch.float32, device=dev) if return_probs else None
+        token_p = token.data_ptr()
+        if return_probs:
+            probs = torch.empty(T, V, dtype=torch.float32, device=dev)
+            probs_p = probs.data_ptr()
     else:
         token, probs = out if return_probs else (out, None)
-        _vec(token, torch.int32, (T,), "out token", dev)
-        if probs is not None:
-            _vec(probs, torch.float32, (T, V), "out probs", dev)
-    _launch(_lib.spec_sample, "spec_sample", dev, stream, logits.data_ptr(), _LOGITS[logits.dtype], T, V,
-            _a(temperature), _a(top_k), _a(top_p), _a(min_p), u.data_ptr(), token.data_ptr(), _a(probs))
+        token_p = _vec(token, torch.int32, (T,), "out token", dev)
+        if return_probs:
+            probs_p = _vec(probs, torch.float32, (T, V), "out probs", dev)
+    _launch(_lib.spec_sample, "spec_sample", dev, stream, logits.data_ptr(), _LOGITS[logits.dtype], T, V, *filters,
+            u_p, token_p, probs_p)
     return (token, probs) if return_probs else token
 
 
@@ -414,21 +414,20 @@ def verify_sample(logits: torch.Tensor, draft: torch.Tensor, u: torch.Tensor, te
     B, K1, V = _rows(logits, "logits", 3)
     K = K1 - 1
     dev = logits.device
-    _vec(draft, torch.int32, (B, K), "draft", dev)
-    _vec(u, torch.float32, (B, K1), "u", dev)
-    _filters(B, dev, temperature, top_k, top_p, min_p)
-    if draft_probs is not None:
-        _vec(draft_probs, torch.float32, (B, K, V), "draft_probs", dev)
+    draft_p = _vec(draft, torch.int32, (B, K), "draft", dev)
+    u_p = _vec(u, torch.float32, (B, K1), "u", dev)
+    filters = _filters(B, dev, temperature, top_k, top_p, min_p)
+    q_p = None if draft_probs is None else _vec(draft_probs, torch.float32, (B, K, V), "draft_probs", dev)
     if out is None:
         cm = torch.empty(B, K1, dtype=torch.int32, device=dev)
         n = torch.empty(B, dtype=torch.int32, device=dev)
+        cm_p, n_p = cm.data_ptr(), n.data_ptr()
     else:
         cm, n = out
-        _vec(cm, torch.int32, (B, K1), "out[0]", dev)
-        _vec(n, torch.int32, (B,), "out[1]", dev)
+        cm_p = _vec(cm, torch.int32, (B, K1), "out[0]", dev)
+        n_p = _vec(n, torch.int32, (B,), "out[1]", dev)
     _launch(_lib.spec_verify_sample, "spec_verify_sample", dev, stream, logits.data_ptr(), _LOGITS[logits.dtype],
-            draft.data_ptr() if K else None, _a(draft_probs), _a(temperature), _a(top_k), _a(top_p), _a(min_p),
-            u.data_ptr(), B, K, V, cm.data_ptr(), n.data_ptr())
+            draft_p if K else None, q_p, *filters, u_p, B, K, V, cm_p, n_p)
     return cm, n
 
 
