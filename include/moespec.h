@@ -122,16 +122,17 @@ MS_API ms_status moe_route_topk_tensor(const void* xhat, const float* w_router, 
  *   topk_idx: the k largest c of those groups, descending, equal values to the
  *   lower expert;  topk_w: s of the chosen experts (the bias only selects),
  *   divided by their sum when renormalize != 0, times scale.
- * Scores and selection are computed in fp64, so the choice does not depend on
- * fp32 rounding.  A logit of -inf or NaN masks its expert: s = 0, ranked
- * behind every other expert of the chosen groups (a masked expert counts 0 in
- * its group's score, a group without any other expert ranks last), so that
- * topk_idx always holds k different experts of the chosen groups, as
- * moe_permute needs.  The bias is finite.
+ * The choice is that of scores in fp64: it does not depend on fp32 rounding.
+ * topk_w is evaluated in fp32 (about 1e-6 relative).  A logit of -inf or NaN
+ * masks its expert: s = 0, ranked behind every other expert of the chosen
+ * groups (a masked expert counts 0 in its group's score, a group without any
+ * other expert ranks last), so that topk_idx always holds k different experts
+ * of the chosen groups, as moe_permute needs.  A bias of -inf or NaN ranks its
+ * expert with the masked ones and leaves it its s.
  * logits: [T,E] fp32 or bf16 (any element alignment).  select_bias: [E] fp32
- * or NULL.  topk_idx:
- * [T,k] int32.  topk_w: [T,k] fp32.  E <= 256, E % n_groups == 0, n_groups <=
- * 32, k <= 32, k <= topk_groups * E / n_groups.  No scratch. */
+ * or NULL.  topk_idx: [T,k] int32.  topk_w: [T,k] fp32.
+ * E <= 256, E % n_groups == 0, n_groups <= 32, k <= 32,
+ * k <= topk_groups * E / n_groups.  No scratch. */
 MS_API ms_status moe_route_grouped(const void* logits, ms_dtype logits_dtype, const float* select_bias, int T, int E,
                                    ms_score score, int n_groups, int topk_groups, int group_top, int k,
                                    int renormalize, float scale, int32_t* topk_idx, float* topk_w, void* stream);
@@ -255,9 +256,10 @@ MS_API ms_status spec_verify_greedy(const void* logits, ms_dtype logits_dtype, c
  * or NaN, min_p <= 0 or NaN leave their filter out; min_p > 1 counts as 1,
  * top_p <= 0 keeps one token.  Tokens at +inf share the whole weight.  A row
  * without any logit above -inf gives token -1 and probabilities 0.
- * temperature is finite; u lies in [0, 1).
- * logits: [T,V] fp32 or bf16 (any element alignment).  temperature, top_p, min_p, u: [T] fp32, top_k:
- * [T] int32; each but u may be NULL (temperature 1, filter left out).
+ * Positive temperatures are clamped to [1e-30, FLT_MAX], u to [0, 1 - 2^-24].
+ * logits: [T,V] fp32 or bf16 (any element alignment).  temperature, top_p,
+ * min_p, u: [T] fp32, top_k: [T] int32; each but u may be NULL (temperature 1,
+ * filter left out).
  * token: [T] int32.  probs: [T,V] fp32 or NULL.  V <= 262,144, T <= 2^24.
  * No scratch. */
 MS_API ms_status spec_sample(const void* logits, ms_dtype logits_dtype, int T, int V, const float* temperature,
@@ -280,9 +282,9 @@ MS_API ms_status spec_sample(const void* logits, ms_dtype logits_dtype, int T, i
  * n_committed[b] = how many of them are tokens: 1..K+1 (one less where the
  * drawn row has no logit above -inf: its token is -1).  A draft outside [0, V)
  * is rejected.
- * logits: [B,K+1,V] fp32 or bf16 (any element alignment).  draft: [B,K] int32.  draft_probs: [B,K,V]
- * fp32 or NULL.  temperature, top_p, min_p: [B] fp32, top_k: [B] int32, each
- * NULL or as in spec_sample.  u: [B,K+1] fp32 in [0, 1), independent.
+ * logits: [B,K+1,V] fp32 or bf16 (any element alignment).  draft: [B,K]
+ * int32.  draft_probs: [B,K,V] fp32 or NULL.  temperature, top_p, min_p: [B]
+ * fp32, top_k: [B] int32, each NULL or as in spec_sample.  u: [B,K+1] fp32 in [0, 1), independent.
  * committed: [B,K+1] int32.  n_committed: [B] int32.  K = 0 (draft may be
  * NULL) is plain sampling.  K <= 8, V <= 262,144, B*(K+1) <= 2^24.
  * No scratch. */

@@ -20,6 +20,7 @@ def distribution(l, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     if not temperature > 0:
         w[int(l.argmax())] = 1.0
         return w
+    temperature = min(max(temperature, 1e-30), float(np.finfo(np.float32).max))
     with np.errstate(invalid="ignore"):
         d = np.where(l == top, 0.0, l - top)
     w = np.exp(d / temperature)
@@ -100,13 +101,14 @@ def route(logits, k, score="softmax", bias=None, n_groups=1, topk_groups=None, g
                 s[on] = np.where(z[on] == top, 1.0, np.exp(z[on] - top if np.isfinite(top) else np.full(on.sum(), -np.inf)))
                 s /= s.sum()
         c = s + (0.0 if bias is None else np.asarray(bias, np.float64))
+        c[~on | np.isnan(c)] = -np.inf   # a NaN bias ranks its expert as a masked one
         ranks = []
         for g in range(n_groups):
-            best = sorted((c[e] for e in range(g * gs, (g + 1) * gs) if on[e]), reverse=True)[:group_top]
+            best = sorted((c[e] for e in range(g * gs, (g + 1) * gs) if c[e] > -np.inf), reverse=True)[:group_top]
             ranks.append((-sum(best) if best else np.inf, g))
         groups = {g for _, g in sorted(ranks)[: topk_groups or n_groups]}
         open_ = [e for e in range(E) if e // gs in groups]
-        chosen = sorted(open_, key=lambda e: (not on[e], -c[e] if on[e] else 0.0, e))[:k]
+        chosen = sorted(open_, key=lambda e: (-c[e], e))[:k]
         idx[t] = chosen
         w[t] = s[chosen]
         if renormalize:

@@ -123,7 +123,8 @@ __device__ __noinline__ void route_token_exact(const RouteGroupedArgs& a, int t,
         const bool on = z[i] > -INFINITY;
         const double v = s[i] * norm;
         score[e] = v;
-        sel[e] = on ? (a.bias ? v + static_cast<double>(__ldg(a.bias + e)) : v) : -INFINITY;
+        const double c = on ? (a.bias ? v + static_cast<double>(__ldg(a.bias + e)) : v) : -INFINITY;
+        sel[e] = c == c ? c : -INFINITY;   // (a NaN bias)
     }
     __syncwarp();
     const int gs = a.E / a.groups;
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4) route_grouped_
             if (a.bias) close |= has && eo != e && fabsf(co - c) < 1.2e-6f + fabsf(c) * 3e-7f;
         }
     }
-    odd |= sub < a.k && !has;
+    odd |= (sub < a.k && !has) || !(c == c);
     unsigned odds = __ballot_sync(0xffffffffu, odd);
     const unsigned closes = __ballot_sync(0xffffffffu, close);
     const unsigned mine = 0xffu << (lane & 24);
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4) route_grouped_
         }
         const int total = __shfl_sync(0xffffffffu, at, (lane & 24) + 7);
         at -= n;
-        const bool fits = total <= 16;
+        const bool fits = total <= 16 && total >= a.k;   // (fewer: infinite or NaN scores by the bias)
         odds |= __ballot_sync(0xffffffffu, !fits && ((closes & mine) != 0));
         if (fits)
             for (uint32_t b = may; b; b &= b - 1) sc.e[at++] = e0 + __ffs(b) - 1;

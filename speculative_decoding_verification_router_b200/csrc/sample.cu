@@ -1569,7 +1569,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
         r.ua = static_cast<double>(__ldg(a.u + static_cast<size_t>(seq) * a.per + pj));
     }
     r.us = static_cast<double>(__ldg(a.u + (VERIFY ? static_cast<size_t>(seq) * a.per + a.per - 1 : static_cast<size_t>(row))));
-    r.us = fmin(r.us, 1.0 - 0x1p-24);
+    r.us = fmax(fmin(r.us, 1.0 - 0x1p-24), 0.0);   // (NaN: the largest)
 
     // ---- the row's part into shared memory, and its maximum
     SpChunk<TL> ck;
@@ -1633,7 +1633,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
         m = fmaxf(m, sm.cmax[i]);
         low = fminf(low, sm.cmin[i]);
     }
-    T = fmax(T, 1e-30);
+    T = fmin(fmax(T, 1e-30), static_cast<double>(FLT_MAX));
     const double c = 1.4426950408889634 / T;
     const SpScale sc{m, scaled_f64(m), c * 0x1p896, c, sm.tab};
     double dmin = -44.361419555836498 * T;   // 64 ln 2
@@ -1713,6 +1713,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
             if (r.by_p) {
                 const float kth = r.by_k ? composite_value(cut) : lcut;
                 if (r.by_k) {
+                    if (!dropped) cluster_sync_warp0();   // the other CTAs have read refine()'s counts (tie_index() waits too)
                     clear_counts(sm);
                     nu = nucleus<TL>(sm, ck, sc, rank, C, kth, r.p, static_cast<double>(dropped) * sc.weight(kth));
                 }

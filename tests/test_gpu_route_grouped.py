@@ -82,6 +82,70 @@ def test_close_scores_are_told_apart(ms):
     _check(ms, z, 6, "f32", bias=bias, score="sigmoid")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,tg,k", [(64, 1, 1, 6), (64, 1, 1, 1), (64, 8, 3, 8), (256, 8, 4, 8), (60, 4, 2, 12)])
+@pytest.mark.parametrize("values", [[np.inf], [-np.inf], [np.nan], [np.inf, -np.inf, np.nan, 0.0]])
+def test_infinite_and_nan_bias(ms, values, E, groups, tg, k, score):
+    g = np.random.default_rng(E + k)
+    z = 2 * g.standard_normal((33, E)).astype(np.float32)
+    for share in (0.02, 0.3, 0.97):
+        bias = (0.1 * g.standard_normal(E)).astype(np.float32)
+        at = g.random(E) < share
+        at[5] = True
+        bias[at] = g.choice(np.array(values, np.float32), int(at.sum()))
+        _check(ms, z, k, "f32", bias=bias, score=score, n_groups=groups, topk_groups=tg, group_top=2, renormalize=True)
+
+
+def _route_many(z, k, score, bias, groups, tg, top):
+    """The definition over whole tensors, in fp64, for finite logits: (idx, renormalised w, whether every decision is
+    by more than 1e-13, ten times the error of a score, or a tie of equal logits)."""
+    T, E = z.shape
+    z = z.double()
+    s = torch.softmax(z, -1) if score == "softmax" else 1.0 / (1.0 + torch.exp(-z))
+    c = s if bias is None else s + bias.double()
+    best = c.view(T, groups, E // groups).sort(-1, descending=True).values[..., :top].sum(-1)
+    keep = torch.zeros(T, groups, dtype=torch.bool, device=z.device)
+    ranked = best.sort(dim=-1, descending=True, stable=True)
+    keep.scatter_(1, ranked.indices[:, :tg], True)
+    c = c.masked_fill(~keep.repeat_interleave(E // groups, 1), -float("inf"))
+    order = c.sort(dim=-1, descending=True, stable=True)
+    idx = order.indices[:, :k]
+    w = s.gather(1, idx)
+    clear = lambda hi, lo: (hi - lo > 1e-13) | ((hi == lo) if bias is None else hi > hi)   # noqa: E731
+    sure = clear(order.values[:, :k], order.values[:, 1: k + 1] if k < E else
+                 torch.cat([order.values[:, 1:], torch.full_like(c[:, :1], -1.0)], 1)).all(1)
+    if tg < groups:
+        sure &= clear(ranked.values[:, tg - 1], ranked.values[:, tg])
+    return idx.int(), w / w.sum(-1, keepdim=True), sure
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(8, 8), (40, 4), (64, 1), (64, 8), (96, 2), (160, 4), (256, 1), (256, 8)])
+def test_many_tokens_with_close_scores(ms, E, groups, score, dtype):
+    """Enough tokens that coarse scores often fail to tell experts or groups apart: random logits, rounded ones (ties),
+    logits within 2^-14 of each other, and wider ones."""
+    T = 20000
+    g = torch.Generator(device="cuda").manual_seed(E + groups)
+    z = 1.5 * torch.randn(T, E, generator=g, device="cuda")
+    z[: T // 4] = torch.round(z[: T // 4] * 8) / 8 + 0.046875
+    near = z[T // 4: T // 2]
+    near.copy_(0.25 + torch.rand(near.shape, generator=g, device="cuda") * 2.0 ** -14)
+    z[-500:] *= 4
+    z = z.to(DTYPES[dtype])
+    tg = max(1, groups // 2)
+    for bias in (None, 0.1 * torch.randn(E, generator=g, device="cuda")):
+        for top in (1, 2):
+            k = min(8, tg * (E // groups))
+            idx, w = ms.route_grouped(z, k, score=score, bias=bias, n_groups=groups, topk_groups=tg, group_top=top,
+                                      renormalize=True)
+            ri, rw, sure = _route_many(z, k, score, bias, groups, tg, top)
+            wrong = sure & (idx != ri).any(1)
+            assert int(wrong.sum()) == 0, (top, bias is not None, wrong.nonzero()[:3].tolist())
+            assert int(sure.sum()) > 0.98 * T
+            assert bool(((w.double() - rw).abs() <= REL * rw + 1e-37)[sure].all())
+
+
 def test_softmax_without_groups_is_route_topk(ms):
     g = np.random.default_rng(1)
     H, E, T = 256, 64, 50

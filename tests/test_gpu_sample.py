@@ -195,6 +195,85 @@ def test_sample_on_another_stream_and_captured(ms):
         assert torch.equal(tok, ms.sample(z, u, top_p=top_p))
 
 
+def test_extreme_temperatures(ms):
+    V, ts = 5000, [1e-38, 1e-30, 1e-20, 1e20, 1e38, np.inf]
+    g = np.random.default_rng(3)
+    for dtype in DTYPES:
+        for kinds in (["normal", "tiny", "two", "masked", "huge", "lowest"], ["inf", "nan", "zeros", "peaked", "one", "empty"]):
+            for ps in (dict(), dict(top_p=0.9), dict(top_k=3000, top_p=0.5), dict(min_p=0.3)):
+                z = np.stack([_row(g, k, V) for k in kinds for _ in ts]).astype(np.float32)
+                t = torch.from_numpy(z).to(DTYPES[dtype])
+                n, u = len(z), _uniform(g, len(z))
+                par = {k: np.full(n, v, np.int32 if k == "top_k" else np.float32) for k, v in ps.items()}
+                par["temperature"] = np.array(ts * len(kinds), np.float32)
+                tok, probs = ms.sample(t.cuda(), dev(u), **_on(par), return_probs=True)
+                with np.errstate(all="ignore"):
+                    want, wp = sp.sample(t.float().numpy(), u, **par)
+                np.testing.assert_array_equal(host(tok), want)
+                _assert_probs(host(probs), wp)
+
+
+def test_random_numbers_outside_their_range_are_clamped(ms):
+    z = torch.randn(4, 9000, device="cuda")
+    top_k = torch.tensor([0, 50, 0, 50], dtype=torch.int32, device="cuda")
+    a = ms.sample(z, torch.tensor([-1.0, -1.0, 7.0, float("nan")], device="cuda"), top_k=top_k)
+    b = ms.sample(z, torch.tensor([0.0, 0.0, 1 - 2.0 ** -24, 1 - 2.0 ** -24], device="cuda"), top_k=top_k)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sample_from_any_element_offset(ms, dtype):
+    """Rows and outputs that start at any element, filters that take every path."""
+    R, V = 6, 10007
+    g = torch.Generator(device="cuda").manual_seed(4)
+    z = (3 * torch.randn(R, V, generator=g, device="cuda")).to(DTYPES[dtype])
+    u = torch.rand(R, generator=g, device="cuda")
+    par = dict(temperature=torch.tensor([1, 1, 2, 2, 3, 1.0], device="cuda"),
+               top_k=torch.tensor([0, 30, 0, 4000, 0, 0], dtype=torch.int32, device="cuda"),
+               top_p=torch.tensor([1, 1, 0.95, 0.9, 0.999, 1], device="cuda"),
+               min_p=torch.tensor([0, 0, 0, 0, 0, 0.01], device="cuda"))
+    tok, probs = ms.sample(z, u, **par, return_probs=True)
+    for shift in range(1, 8):
+        zs = torch.empty(R * V + 8, dtype=z.dtype, device="cuda")[shift: shift + R * V].view(R, V).copy_(z)
+        out = torch.full((R * V + 16,), 7.0, device="cuda")
+        t = torch.empty(R, dtype=torch.int32, device="cuda")
+        ms.sample(zs, u, **par, return_probs=True, out=(t, out[shift: shift + R * V].view(R, V)))
+        assert torch.equal(t, tok) and torch.equal(out[shift: shift + R * V].view(R, V), probs)
+        assert bool((out[:shift] == 7).all()) and bool((out[shift + R * V:] == 7).all())
+
+
+def test_offsets_beyond_32_bits(ms):
+    R, V = 8250, 262144            # 2.16e9 logits and probabilities
+    g = torch.Generator(device="cuda").manual_seed(6)
+    z = torch.zeros(R, V, dtype=torch.bfloat16, device="cuda")
+    z[-40:].normal_(generator=g).mul_(2)
+    u = torch.rand(R, generator=g, device="cuda")
+    top_k = torch.tensor([0, 20, 5000, 0] * (R // 4) + [20, 20], dtype=torch.int32, device="cuda")
+    tok, probs = ms.sample(z, u, top_k=top_k, return_probs=True)
+    t, p = ms.sample(z[-40:].clone(), u[-40:], top_k=top_k[-40:], return_probs=True)
+    assert torch.equal(tok[-40:], t) and torch.equal(probs[-40:], p)
+    want, _ = sp.sample(host(z[-2:].float()), host(u[-2:]), top_k=host(top_k[-2:]))
+    np.testing.assert_array_equal(host(t[-2:]), want)
+    del z, probs
+
+
+def test_two_streams_at_once(ms):
+    R, V = 64, 50000
+    z = [torch.randn(R, V, device="cuda") * (1 + i) for i in range(2)]
+    u = torch.rand(R, device="cuda")
+    top_p = torch.full((R,), 0.95, device="cuda")
+    want = [ms.sample(x, u, top_p=top_p, return_probs=True) for x in z]
+    streams = [torch.cuda.Stream() for _ in z]
+    out = [(torch.empty(R, dtype=torch.int32, device="cuda"), torch.empty(R, V, device="cuda")) for _ in z]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for x, s, o in zip(z, streams, out):
+            ms.sample(x, u, top_p=top_p, return_probs=True, out=o, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(out, want):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+
+
 # ---------------------------------------------------------------- verification
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -306,6 +385,44 @@ def test_verify_sample_captured(ms):
         torch.cuda.synchronize()
         cm, n = ms.verify_sample(z, d, u, top_k=k)
         assert torch.equal(out[0], cm) and torch.equal(out[1], n)
+
+
+def test_draft_probs_beyond_32_bits(ms):
+    B, K, V = 1040, 8, 262144      # 2.18e9 draft probabilities, 2.45e9 logits
+    z = torch.zeros(B, K + 1, V, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(B, K, V, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    z[-2:].normal_(generator=g).mul_(3)
+    d = z[:, :K].argmax(-1).int()
+    q[-2:] = torch.softmax(z[-2:, :K].float() + 0.5 * torch.randn(2, K, V, generator=g, device="cuda"), -1)
+    u = 0.7 * torch.rand(B, K + 1, generator=g, device="cuda")
+    top_p = torch.full((B,), 0.9, device="cuda")
+    cm, n = ms.verify_sample(z, d, u, top_p=top_p, draft_probs=q)
+    want = ms.verify_sample(z[-2:].clone(), d[-2:], u[-2:], top_p=top_p[-2:], draft_probs=q[-2:].clone())
+    assert torch.equal(cm[-2:], want[0]) and torch.equal(n[-2:], want[1])
+    wcm, wn = sp.verify(host(z[-1:].float()), host(d[-1:]), host(u[-1:]), host(q[-1:]), top_p=host(top_p[-1:]))
+    np.testing.assert_array_equal(host(cm[-1:]), wcm)
+    np.testing.assert_array_equal(host(n[-1:]), wn)
+
+
+def test_verify_two_graphs_with_draft_probs(ms):
+    """Two captured graphs of the same inputs, replayed at once, each on its own stream."""
+    B, K, V = 6, 2, 20011
+    z = 2 * torch.randn(B, K + 1, V, device="cuda")
+    q = torch.softmax(z[:, :K] + torch.randn(B, K, V, device="cuda"), -1)
+    u, d = torch.rand(B, K + 1, device="cuda"), z[:, :K].argmax(-1).int()
+    outs = [(torch.empty(B, K + 1, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda"))
+            for _ in range(2)]
+    graphs = [ms.CapturedStep(lambda o=o: ms.verify_sample(z, d, u, draft_probs=q, out=o)) for o in outs]
+    for seed in range(4):
+        u.uniform_(generator=torch.Generator(device="cuda").manual_seed(seed))
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph()
+        torch.cuda.synchronize()
+        cm, n = ms.verify_sample(z, d, u, draft_probs=q)
+        for o in outs:
+            assert torch.equal(o[0], cm) and torch.equal(o[1], n)
 
 
 def test_draft_head_sampled_verify_chain(ms):
