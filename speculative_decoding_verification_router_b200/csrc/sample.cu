@@ -140,6 +140,20 @@ __device__ __forceinline__ T warp_scan(T v, int lane) {   // inclusive
     return v;
 }
 
+// Sum of the lower lanes' v <= 15, and of all lanes': a ballot per bit, which do
+// not wait for one another as the steps of a scan do.
+__device__ __forceinline__ uint32_t lanes_before(uint32_t v, int lane, uint32_t& all) {
+    uint32_t before = 0;
+    all = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t bits = __ballot_sync(0xffffffffu, (v >> i) & 1u);
+        before += __popc(bits & ((1u << lane) - 1u)) << i;
+        all += __popc(bits) << i;
+    }
+    return before;
+}
+
 // The elements of a 16-byte vector.
 template <typename TL>
 struct SpElem;
@@ -164,6 +178,10 @@ struct SpElem<float> {
     static __device__ __forceinline__ bool all_ge(const uint4& r, Bound t) {
         return __uint_as_float(r.x) >= t && __uint_as_float(r.y) >= t && __uint_as_float(r.z) >= t &&
                __uint_as_float(r.w) >= t;
+    }
+    static __device__ __forceinline__ bool any_eq(const uint4& r, float t) {
+        return __uint_as_float(r.x) == t || __uint_as_float(r.y) == t || __uint_as_float(r.z) == t ||
+               __uint_as_float(r.w) == t;
     }
     struct Max {
         float m = -INFINITY;
@@ -210,6 +228,11 @@ struct SpElem<__nv_bfloat16> {
     static __device__ __forceinline__ bool all_ge(const uint4& r, Bound t) {
         return __hbge2(__hmin2_nan(__hmin2_nan(pair(r.x), pair(r.y)), __hmin2_nan(pair(r.z), pair(r.w))), t);
     }
+    static __device__ __forceinline__ bool any_eq(const uint4& r, float t) {
+        const __nv_bfloat162 x = __float2bfloat162_rn(t);
+        return (__heq2_mask(pair(r.x), x) | __heq2_mask(pair(r.y), x) | __heq2_mask(pair(r.z), x) |
+                __heq2_mask(pair(r.w), x)) != 0;
+    }
     struct Max {
         __nv_bfloat162 m = __halves2bfloat162(__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80));
         __device__ __forceinline__ void add(const uint4& r) {
@@ -226,7 +249,7 @@ struct SampleSmem {
     double tab[16], ptab[16];                 // 2^(j/16), and the same over the row's sum
     double wsum[SP_MAXC * SP_WARPS];          // every warp's sum, of every CTA of the cluster
     double rsum[SP_MAXC * SP_WARPS];          // the same for the residual
-    double dscan[SP_WARPS];
+    double dscan[2][SP_WARPS];
     float fscan[2][SP_WARPS];
     unsigned long long scan[SP_WARPS];
     unsigned long long sel_key;
@@ -304,6 +327,27 @@ __device__ void share_sums(double* sums, double s, uint32_t rank, uint32_t C) {
     if (warp == 0)
         for (int i = lane; i < static_cast<int>(C) * SP_WARPS; i += 32)
             if (static_cast<uint32_t>(i) / SP_WARPS != rank) st_cluster_f64(own + i % SP_WARPS, i / SP_WARPS, own[i % SP_WARPS]);
+    cluster_sync_warp0();
+}
+
+// The same for two tables at once.
+__device__ void share_two(double* ta, double a, double* tb, double b, uint32_t rank, uint32_t C) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    a = warp_sum_f64(a);
+    b = warp_sum_f64(b);
+    ta += rank * SP_WARPS;
+    tb += rank * SP_WARPS;
+    if (lane == 0) {
+        ta[warp] = a;
+        tb[warp] = b;
+    }
+    __syncthreads();
+    if (warp == 0)
+        for (int i = lane; i < static_cast<int>(C) * SP_WARPS; i += 32)
+            if (static_cast<uint32_t>(i) / SP_WARPS != rank) {
+                st_cluster_f64(ta + i % SP_WARPS, i / SP_WARPS, ta[i % SP_WARPS]);
+                st_cluster_f64(tb + i % SP_WARPS, i / SP_WARPS, tb[i % SP_WARPS]);
+            }
     cluster_sync_warp0();
 }
 
@@ -594,13 +638,12 @@ __device__ uint32_t gather(SampleSmem& sm, uint32_t* ccnt, const SpChunk<TL>& ck
             SpElem<TL>::unpack(raw, v);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) mask |= (v[e] >= floor && keep(v[e]) ? 1u : 0u) << e;
-            const uint32_t mine = __popc(mask);
-            const uint32_t in = warp_scan(mine, lane);
-            uint32_t w = at + in - mine;
+            uint32_t all;
+            uint32_t w = at + lanes_before(__popc(mask), lane, all);
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
                 if (mask & (1u << e)) sm.loc[w++] = composite(v[e], ck.index(v0 + lane, e));
-            at += __shfl_sync(0xffffffffu, in, 31);
+            at += all;
         }
     }
     cluster_sync_warp0();
@@ -653,16 +696,36 @@ __device__ __forceinline__ void block_runs(SampleSmem& sm, double own, int nwarp
     double prev = __shfl_up_sync(0xffffffffu, inc, 1);
     if (lane == 0) prev = 0.0;
     __syncthreads();
-    if (lane == 31) sm.dscan[warp] = inc;
+    if (lane == 31) sm.dscan[0][warp] = inc;
     __syncthreads();
     double base = 0.0, sum = 0.0;
     for (int w = 0; w < nwarps; ++w) {
         if (w == warp) base = sum;
-        sum += sm.dscan[w];
+        sum += sm.dscan[0][w];
     }
     start = base + prev;
     end = base + inc;
     total = sum;
+}
+
+// The starts of two sets of runs at once.
+__device__ __forceinline__ void block_starts(SampleSmem& sm, double a, double b, double& sa, double& sb) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const double ia = warp_scan(a, lane), ib = warp_scan(b, lane);
+    double pa = __shfl_up_sync(0xffffffffu, ia, 1), pb = __shfl_up_sync(0xffffffffu, ib, 1);
+    if (lane == 0) pa = pb = 0.0;
+    if (lane == 31) {
+        sm.dscan[0][warp] = ia;
+        sm.dscan[1][warp] = ib;
+    }
+    __syncthreads();
+    sa = sb = 0.0;
+    for (int w = 0; w < warp; ++w) {
+        sa += sm.dscan[0][w];
+        sb += sm.dscan[1][w];
+    }
+    sa += pa;
+    sb += pb;
 }
 
 constexpr int SP_PER = SP_CAP / SP_THREADS;
@@ -1070,64 +1133,290 @@ __device__ void draw_from_list(SampleSmem& sm, int n, int ksh, float lcut, const
     if (e >= 0) *token = composite_index(lst[tid * per + e]);
 }
 
+// ---------------------------------------------------------------- borders by counting every value (bf16)
+// A bf16 row has few distinct values: between the smallest and the largest that
+// carry weight there are at most some thousands, but for the many tiny ones
+// around zero.  One pass counts each (the values of magnitude at most m0 as one,
+// their weights summed apart); counts times weights are then exact sums in the
+// order of the selection, and the borders of top-k and top-p follow by a scan.
+constexpr int SP_KEYS = 4096;
+static_assert(SP_KEYS * sizeof(uint32_t) <= sizeof(SampleSmem::lst), "the counts share the candidates' memory");
+constexpr int SP_KPT = SP_KEYS / SP_THREADS;
+
+struct SpKeys {
+    int m0, top, n;   // value of rank r below the maximum: signed magnitude top - r, less the collapsed ones
+    static __device__ __forceinline__ int signed_mag(float l) {
+        const int b = __float_as_int(l) >> 16;   // (sign-extended)
+        return b < 0 ? -(b & 0x7fff) : b;
+    }
+    __device__ __forceinline__ int squeeze(int s) const { return s > m0 ? s - m0 : s < -m0 ? s + m0 : 0; }
+    // NaN and what lies below the smallest get ranks of n and more (as unsigned)
+    __device__ __forceinline__ uint32_t rank(uint32_t bits, uint32_t sign) const {   // 15 bits, 0 or ~0
+        const uint32_t a = max(static_cast<int>(bits) - m0, 0);
+        return top + sign - (a ^ sign);
+    }
+    __device__ __forceinline__ uint32_t rank(float l) const { return static_cast<uint32_t>(top - squeeze(signed_mag(l))); }
+    __device__ __forceinline__ bool mixed(uint32_t r) const { return m0 > 0 && static_cast<int>(r) == top; }
+    __device__ __forceinline__ float value(uint32_t r) const {
+        const int c = top - static_cast<int>(r), s = c > 0 ? c + m0 : c < 0 ? c - m0 : 0;
+        return __uint_as_float(static_cast<uint32_t>(s < 0 ? 0x8000 - s : s) << 16);
+    }
+};
+// The values from m down to lo, bf16 both; the smallest m0 that fits.
+__device__ __forceinline__ SpKeys make_keys(float m, float lo) {
+    const int a = SpKeys::signed_mag(m), b = SpKeys::signed_mag(lo);
+    SpKeys k{a - b < SP_KEYS ? 0 : max((a - b + 2 - SP_KEYS) >> 1, max(a, -b) + 1 - SP_KEYS), 0, 0};
+    k.top = k.squeeze(a);
+    k.n = k.top - k.squeeze(b) + 1;
+    return k;
+}
+
+struct SpBorder {
+    bool ok;               // false: a border among the collapsed values
+    uint32_t r;            // rank of the border's value,
+    uint32_t above, ties;  // tokens above it and with it,
+    uint32_t keep;         // and how many of the latter are kept
+    double zsum;           // this thread's part of the collapsed values' weights
+};
+
+// The border of the first k tokens (k > 0) and, p < 1, of the prefix of those
+// that reaches p times their sum; S > 0: p times S instead.  The border is at or
+// above the smallest of the keys.  All threads of the cluster call it.
+__device__ SpBorder key_border(SampleSmem& sm, const SpChunk<__nv_bfloat16>& ck, const SpScale& sc, const SpKeys& keys,
+                               uint32_t rank, uint32_t C, float lo, uint32_t k, double p, double S) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t* hist = reinterpret_cast<uint32_t*>(sm.lst);
+    for (int i = tid; i < keys.n; i += SP_THREADS) hist[i] = 0;
+    if (tid == 0) {
+        sm.nb0 = SP_KEYS;
+        sm.nb1 = SP_KEYS;
+        sm.last = 0;
+    }
+    __syncthreads();
+    SpBorder o;
+    o.zsum = 0.0;
+    const __nv_bfloat162 small = __halves2bfloat162(__ushort_as_bfloat16(keys.m0), __ushort_as_bfloat16(keys.m0));
+    for (int q = tid; q < ck.nvec; q += SP_THREADS) {
+        const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[q];
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t r0 = keys.rank(w[i] & 0x7fffu, static_cast<uint32_t>(static_cast<int>(w[i] << 16) >> 31));
+            const uint32_t r1 = keys.rank((w[i] >> 16) & 0x7fffu, static_cast<uint32_t>(static_cast<int>(w[i]) >> 31));
+            if (r0 < keys.n) atomicAdd(&hist[r0], 1u);
+            if (r1 < keys.n) atomicAdd(&hist[r1], 1u);
+        }
+        if (keys.m0 > 0) {
+            const __nv_bfloat162 a = __hmin2(__hmin2(__habs2(SpElem<__nv_bfloat16>::pair(raw.x)), __habs2(SpElem<__nv_bfloat16>::pair(raw.y))),
+                                             __hmin2(__habs2(SpElem<__nv_bfloat16>::pair(raw.z)), __habs2(SpElem<__nv_bfloat16>::pair(raw.w))));
+            if (__hle2_mask(a, small)) {
+                float v[8];
+                SpElem<__nv_bfloat16>::unpack(raw, v);
+                for (int e = 0; e < 8; ++e)
+                    if (keys.rank(v[e]) == static_cast<uint32_t>(keys.top) && v[e] >= lo) o.zsum += sc.weight(v[e]);
+            }
+        }
+    }
+    double z = 0.0;
+    if (keys.m0 > 0) {
+        share_sums(sm.rsum, o.zsum, rank, C);
+        z = table_sum(sm.rsum, C, lane);
+    } else {
+        cluster_sync_warp0();
+    }
+    // the cluster's counts, then this thread's ranks, in order
+    uint32_t* sum = reinterpret_cast<uint32_t*>(sm.loc);
+    for (int i = tid; i < keys.n; i += SP_THREADS) {
+        uint32_t x[SP_MAXC], t = 0;
+#pragma unroll
+        for (uint32_t c = 0; c < SP_MAXC; ++c) {
+            x[c] = 0;
+            if (c < C) asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x[c]) : "r"(sp_mapa(&hist[i], c)) : "memory");
+        }
+#pragma unroll
+        for (uint32_t c = 0; c < SP_MAXC; ++c) t += x[c];
+        sum[i] = t;
+    }
+    __syncthreads();
+    const int per = (keys.n + SP_THREADS - 1) / SP_THREADS, r0 = tid * per;
+    uint32_t n[SP_KPT], own = 0;
+    double w[SP_KPT], wown = 0.0, start, end, total;
+#pragma unroll
+    for (int j = 0; j < SP_KPT; ++j) {
+        n[j] = j < per && r0 + j < keys.n ? sum[r0 + j] : 0u;
+        own += n[j];
+    }
+    uint32_t last = 0;
+#pragma unroll
+    for (int j = 0; j < SP_KPT; ++j) {
+        w[j] = 0.0;
+        if (n[j]) {
+            w[j] = keys.mixed(r0 + j) ? z : n[j] * sc.weight(keys.value(r0 + j));
+            last = r0 + j;
+        }
+        wown += w[j];
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0) atomicMax(&sm.last, static_cast<int>(last));
+    uint32_t ex = warp_scan(own, lane);
+    if (lane == 31) sm.wcnt[warp] = ex;
+    block_runs(sm, wown, SP_WARPS, start, end, total);
+    ex -= own;
+    uint32_t all = 0;
+    for (int i = 0; i < SP_WARPS; ++i) {
+        if (i < warp) ex += sm.wcnt[i];
+        all += sm.wcnt[i];
+    }
+    // the k-th token: its value, how many of that value are kept, the sum of the tokens kept
+    uint32_t kr = SP_KEYS, kkeep = 0;
+    if (!(S > 0.0)) S = total;
+    if (k > 0 && k < all) {
+        uint32_t c = ex;
+        double run = start;
+#pragma unroll
+        for (int j = 0; j < SP_KPT; ++j) {
+            if (c < k && c + n[j] >= k) {
+                sm.nb0 = r0 + j;
+                sm.nn = k - c;
+                sm.sel_w = run + w[j] / n[j] * (k - c);
+            }
+            c += n[j];
+            run += w[j];
+        }
+        __syncthreads();
+        kr = sm.nb0;
+        kkeep = sm.nn;
+        S = sm.sel_w;
+        __syncthreads();   // they are written again below
+    }
+    double target = 0.0;
+    uint32_t r = min(kr, static_cast<uint32_t>(sm.last));
+    if (p < 1.0) {
+        target = fmax(p * S, 1e-9);
+        double run = start;
+        uint32_t f = SP_KEYS;
+#pragma unroll
+        for (int j = 0; j < SP_KPT; ++j) {
+            run += w[j];
+            if (n[j] && run >= target) f = min(f, static_cast<uint32_t>(r0 + j));
+        }
+        f = __reduce_min_sync(0xffffffffu, f);
+        if (lane == 0) atomicMin(&sm.nb1, f);
+        __syncthreads();
+        r = min(r, sm.nb1);
+    }
+    double run = start;
+#pragma unroll
+    for (int j = 0; j < SP_KPT; ++j) {
+        if (j < per && r == static_cast<uint32_t>(r0 + j)) {
+            sm.sel_before = run;
+            sm.sel_w = w[j] / n[j];
+            sm.sel_cnt = ex;
+            sm.nn = n[j];
+        }
+        ex += n[j];
+        run += w[j];
+    }
+    __syncthreads();
+    o.r = r;
+    o.above = sm.sel_cnt;
+    o.ties = sm.nn;
+    o.keep = r == kr ? kkeep : o.ties;
+    if (p < 1.0) {
+        const double need = ceil((target - sm.sel_before) / sm.sel_w);
+        if (need < static_cast<double>(o.keep)) o.keep = need < 1.0 ? 1u : static_cast<uint32_t>(need);
+    }
+    o.ok = !keys.mixed(r) && !(kr < SP_KEYS && keys.mixed(kr));
+    return o;
+}
+
+// This thread's part of the kept weights of its CTA: the counted values above
+// the border, `ties` of the border's, without the certain draft's (rank rx).
+__device__ double key_sum(const SampleSmem& sm, const SpScale& sc, const SpKeys& keys, const SpBorder& b, uint32_t ties,
+                          uint32_t rx) {
+    const uint32_t* hist = reinterpret_cast<const uint32_t*>(sm.lst);
+    double s = keys.m0 > 0 && static_cast<uint32_t>(keys.top) < b.r ? b.zsum : 0.0;
+    for (uint32_t r = threadIdx.x; r <= b.r; r += SP_THREADS) {
+        if (keys.mixed(r)) continue;
+        const uint32_t n = (r == b.r ? ties : hist[r]) - (r == rx ? 1u : 0u);
+        if (n) s += n * sc.weight(keys.value(r));
+    }
+    return s;
+}
+
 // ---------------------------------------------------------------- the draw from the whole row
-// Sum of every warp's weights at or above tau into sums[cta][warp] of every CTA
-// (one cluster barrier).
+// This thread's part of its warp's weights at or above tau.
 template <typename TL>
-__device__ void segment_sums(double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float tau,
-                             const SpScale& sc) {
+__device__ double segment_part(const SpChunk<TL>& ck, float tau, const SpScale& sc) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
     double s0 = 0.0, s1 = 0.0;
     const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(tau);
     for (int v0 = q0; v0 < q1; v0 += 32) add_weights<TL>(ck.raw_to(v0 + lane, q1), tau, tb, sc, s0, s1);
-    share_sums(sums, s0 + s1, rank, C);
+    return s0 + s1;
 }
+
+// w - q S, S as S 2^896 (q is 0 or more; an infinite or NaN one leaves nothing).
+__device__ __forceinline__ double residual(double w, float q, double S896) { return fma(-scaled_f64(q), S896, w); }
 
 // One element of the residual max(w - q S, 0) of the weights at or above tau
 // (q NULL: of the weights).
 template <typename TL>
-__device__ __forceinline__ double left_weight(float l, int idx, float tau, const SpScale& sc, const float* q, double S) {
+__device__ __forceinline__ double left_weight(float l, int idx, float tau, const SpScale& sc, const float* q, double S896) {
     if (!(l >= tau)) return 0.0;
     const double w = sc.weight(l);
-    return q ? fmax(0.0, w - static_cast<double>(__ldg(q + idx)) * S) : w;
+    return q ? fmax(0.0, residual(w, __ldg(q + idx), S896)) : w;
 }
 
 template <typename TL>
 __device__ void residual_sums(double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float tau,
-                              const SpScale& sc, const float* q, double S) {
+                              const SpScale& sc, const float* q, double S896) {
     constexpr int VEC = SpElem<TL>::VEC;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
     double s = 0.0;
+    const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(tau);
+    const float* qp = q + ck.begin - ck.mis;   // of the part's first vector
+    const bool wide = ck.mis == 0 && (reinterpret_cast<uintptr_t>(qp) & 15u) == 0;
     for (int v0 = q0 + lane; v0 < q1; v0 += 32) {
-        float v[VEC];
-        ck.load(v0, v);
+        const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[v0];
+        if (wide && (v0 + 1) * VEC <= ck.n && SpElem<TL>::all_ge(raw, tb)) {
+            float4 f[VEC / 4];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s += left_weight<TL>(v[e], ck.index(v0, e), tau, sc, q, S);
+            for (int e = 0; e < VEC / 4; ++e) f[e] = __ldg(reinterpret_cast<const float4*>(qp + v0 * VEC) + e);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float4& g = f[e / 4];
+                const double d = residual(sc.weight(SpElem<TL>::scaled(raw, e), sc.tab),
+                                          e % 4 == 0 ? g.x : e % 4 == 1 ? g.y : e % 4 == 2 ? g.z : g.w, S896);
+                if (d > 0.0) s += d;
+            }
+        } else if (SpElem<TL>::any_ge(raw, tb)) {
+            float v[VEC];
+            SpElem<TL>::unpack(raw, v);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s += left_weight<TL>(v[e], ck.index(v0, e), tau, sc, q, S896);
+        }
     }
     share_sums(sums, s, rank, C);
 }
 
-// The first index whose cumulative weight exceeds u times the total.  Returns
-// the token in the warp that owns it, -1 elsewhere.
+// The first index whose cumulative weight exceeds the target, given the sums of
+// nseg segments, of which this warp has segment `own_seg`.  Returns the token in
+// the warp that owns it, -1 elsewhere.
 template <typename TL>
-__device__ int draw_token(const double* sums, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, float tau,
-                          const SpScale& sc, const float* q, double S, double u) {
+__device__ int draw_token(const double* sums, int nseg, int own_seg, const SpChunk<TL>& ck, float tau, const SpScale& sc,
+                          const float* q, double S896, double target) {
     constexpr int VEC = SpElem<TL>::VEC;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nseg = static_cast<int>(C) * SP_WARPS;
     const int per = (nseg + 31) / 32;
     // every warp finds the owning segment: lane l scans segments [l per, l per + per)
     double own = 0.0;
     for (int j = 0; j < per; ++j)
         if (lane * per + j < nseg) own += sums[lane * per + j];
-    const double inc = warp_scan(own, lane);
-    const double total = __shfl_sync(0xffffffffu, inc, 31);
-    const double target = u * total;
-    double base = inc - own;
+    double base = warp_scan(own, lane) - own;
     int seg = -1, lastseg = -1;
     double seg_base = 0.0, last_base = 0.0;
     for (int j = 0; j < per; ++j) {
@@ -1152,7 +1441,7 @@ __device__ int draw_token(const double* sums, const SpChunk<TL>& ck, uint32_t ra
     }
     seg = __shfl_sync(0xffffffffu, seg, src);
     base = __shfl_sync(0xffffffffu, seg_base, src);
-    if (seg != static_cast<int>(rank) * SP_WARPS + warp) return -1;
+    if (seg != own_seg) return -1;
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
     int last = -1;
@@ -1164,7 +1453,7 @@ __device__ int draw_token(const double* sums, const SpChunk<TL>& ck, uint32_t ra
         ck.load_to(vq, q1, v);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            w[e] = left_weight<TL>(v[e], ck.index(vq, e), tau, sc, q, S);
+            w[e] = left_weight<TL>(v[e], ck.index(vq, e), tau, sc, q, S896);
             s += w[e];
             if (w[e] > 0.0) mine = ck.index(vq, e);
         }
@@ -1270,7 +1559,7 @@ __device__ uint32_t refine(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale&
         cluster_sync_warp0();
         uint32_t n[SP_BPT];
         pull_counts(sm, C, n);
-        double hi[SP_BPT], low[SP_BPT], hown = 0.0, lown = 0.0, hs, he, ls, le, total;
+        double hi[SP_BPT], low[SP_BPT], hown = 0.0, lown = 0.0, hs, ls;
 #pragma unroll
         for (int j = 0; j < SP_BPT; ++j) {
             const uint32_t b = SP_BPT * tid + j;
@@ -1284,8 +1573,7 @@ __device__ uint32_t refine(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale&
             lown += low[j];
             if (n[j]) atomicMax(&sm.last, static_cast<int>(b));
         }
-        block_runs(sm, hown, SP_WARPS, hs, he, total);
-        block_runs(sm, lown, SP_WARPS, ls, le, total);
+        block_starts(sm, hown, lown, hs, ls);
         hs += A;
         ls += A;
         const double from = ls;   // the running sum at this thread's first bin
@@ -1340,9 +1628,8 @@ __device__ uint32_t refine(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale&
             if (key > top) before += x;
             else of += x;
         });
-        share_sums(sm.rsum, before, rank, C);
+        share_two(sm.rsum, before, sm.wsum, of, rank, C);
         before = table_sum(sm.rsum, C, lane);
-        share_sums(sm.wsum, of, rank, C);
         of = table_sum(sm.wsum, C, lane);
         A += before;
         if (A + of >= target || bot == klo || b0 == b1) {
@@ -1354,7 +1641,7 @@ __device__ uint32_t refine(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale&
             khi = bot - 1;
             klo = end - klo > span ? end - span : klo;
         }
-        cluster_sync_warp0();   // the tables have been read
+        // (every CTA has read the counts before share_two()'s barrier, and reads the tables before the next counts')
     }
 }
 
@@ -1373,11 +1660,14 @@ __device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, u
     auto ties_at = [&](int i) -> uint32_t {   // a bit per element of entry or vector i
         if (i >= last) return 0;
         if (win.listed) return composite_value(sm.loc[i]) == tau ? 1u : 0u;
-        float v[VEC];
-        ck.load(i, v);
+        const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[i];
         uint32_t mask = 0;
+        if (SpElem<TL>::any_eq(raw, tau)) {
+            float v[VEC];
+            SpElem<TL>::unpack(raw, v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) mask |= (v[e] == tau ? 1u : 0u) << e;
+            for (int e = 0; e < VEC; ++e) mask |= (v[e] == tau ? 1u : 0u) << e;
+        }
         return mask;
     };
     uint32_t n = 0;
@@ -1398,20 +1688,63 @@ __device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, u
         for (int i0 = first; i0 < last; i0 += 32) {
             uint32_t mask = ties_at(i0 + lane);
             const uint32_t mine = __popc(mask);
-            const uint32_t in = warp_scan(mine, lane);
-            if (in >= left && in - mine < left) {
-                uint32_t skip = left - (in - mine) - 1;
+            uint32_t t;
+            const uint32_t ex = lanes_before(mine, lane, t);
+            if (ex + mine >= left && ex < left) {
+                uint32_t skip = left - ex - 1;
                 while (skip--) mask &= mask - 1;
                 const int idx = win.listed ? composite_index(sm.loc[i0 + lane]) : ck.index(i0 + lane, __ffs(mask) - 1);
                 for (uint32_t r = 0; r < C; ++r) st_cluster_s32(&sm.cut_idx, r, idx);
             }
-            const uint32_t t = __shfl_sync(0xffffffffu, in, 31);
             if (t >= left) break;
             left -= t;
         }
     }
     cluster_sync_all();
     return static_cast<int>(sm.cut_idx);
+}
+
+// Index of the keep-th of this CTA's elements equal to tau.
+template <typename TL>
+__device__ int own_tie(SampleSmem& sm, const SpChunk<TL>& ck, float tau, uint32_t keep) {
+    constexpr int VEC = SpElem<TL>::VEC;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int q0, q1;
+    warp_segment(ck.nvec, warp, q0, q1);
+    auto ties_at = [&](int i) -> uint32_t {
+        if (i >= q1) return 0;
+        const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[i];
+        uint32_t mask = 0;
+        if (SpElem<TL>::any_eq(raw, tau)) {
+            float v[VEC];
+            SpElem<TL>::unpack(raw, v);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) mask |= (v[e] == tau ? 1u : 0u) << e;
+        }
+        return mask;
+    };
+    uint32_t n = 0;
+    for (int i = q0 + lane; i < q1; i += 32) n += __popc(ties_at(i));
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) sm.wcnt[warp] = n;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < warp; ++w) before += sm.wcnt[w];
+    if (keep > before && keep <= before + n) {
+        uint32_t left = keep - before;
+        for (int i0 = q0; i0 < q1; i0 += 32) {
+            uint32_t mask = ties_at(i0 + lane), t;
+            const uint32_t mine = __popc(mask), ex = lanes_before(mine, lane, t);
+            if (ex + mine >= left && ex < left) {
+                for (uint32_t skip = left - ex - 1; skip; --skip) mask &= mask - 1;
+                sm.last = ck.index(i0 + lane, __ffs(mask) - 1);
+            }
+            if (t >= left) break;
+            left -= t;
+        }
+    }
+    __syncthreads();
+    return sm.last;
 }
 
 // The count table of every CTA to zero (one cluster barrier).
@@ -1423,8 +1756,12 @@ __device__ void clear_counts(SampleSmem& sm) {
 // Masks this CTA's elements equal to tau behind index icut.
 template <typename TL>
 __device__ void mask_ties(const SpChunk<TL>& ck, float tau, int icut) {
-    for (int i = max(0, icut + 1 - ck.begin) + threadIdx.x; i < ck.n; i += SP_THREADS)
-        if (static_cast<float>(ck.buf[ck.mis + i]) == tau) ck.buf[ck.mis + i] = SpElem<TL>::ninf();
+    constexpr int VEC = SpElem<TL>::VEC;
+    for (int q = max(0, icut + 1 - ck.begin + ck.mis) / VEC + threadIdx.x; q < ck.nvec; q += SP_THREADS) {
+        if (!SpElem<TL>::any_eq(reinterpret_cast<const uint4*>(ck.buf)[q], tau)) continue;
+        for (int e = 0; e < VEC; ++e)
+            if (ck.index(q, e) > icut && static_cast<float>(ck.buf[q * VEC + e]) == tau) ck.buf[q * VEC + e] = SpElem<TL>::ninf();
+    }
 }
 
 // This thread's sum of the weights at or above lo in intervals before b0.
@@ -1638,7 +1975,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
     const SpScale sc{m, scaled_f64(m), c * 0x1p896, c, sm.tab};
     double dmin = -44.361419555836498 * T;   // 64 ln 2
     if (mp > 0.0) dmin = fmax(dmin, T * log(fmin(mp, 1.0)));
-    const float lcut = fmaxf(__double2float_ru(static_cast<double>(m) + dmin), -FLT_MAX);
+    float lcut = fmaxf(__double2float_ru(static_cast<double>(m) + dmin), -FLT_MAX);
 
     if (m == -INFINITY) {   // nothing can be drawn
         if (rank == 0 && tid == 0) a.token[row] = -1;
@@ -1663,6 +2000,28 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
         if (nu.n <= SP_CAP) {
             const SpBins bins = first_bins(sc, lcut);
             n = gather<TL>(sm, ccnt = sm.ccnt[1], ck, rank, C, bins.lower(nu.b1, lcut), [&](float l) { return bins.of(l) <= nu.b1; });
+        }
+    }
+    bool counted = false;   // bf16: the border is known from counts
+    SpKeys keys{};
+    SpBorder kb{};
+    if constexpr (SpElem<TL>::KSH == 16) {
+        if (n > SP_CAP && (r.by_k || r.by_p)) {
+            const float lo = r.by_k ? lcut : first_bins(sc, lcut).lower(nu.b1, lcut);
+            keys = make_keys(m, __bfloat162float(__float2bfloat16_ru(lo)));
+            // (not with a cut or a certain draft among the collapsed values)
+            bool can = !keys.mixed(keys.n - 1);
+            if (VERIFY && r.x >= 0 && !r.q) can = can && !keys.mixed(keys.rank(static_cast<float>(rowp[r.x])));
+            if (can) kb = key_border(sm, ck, sc, keys, rank, C, lo, r.by_k ? static_cast<uint32_t>(r.k) : 0u, r.p, nu.S);
+            counted = can && kb.ok;
+            if (counted) {   // what is left is to keep the first tokens down to the border
+                lcut = keys.value(kb.r);
+                r.by_p = false;
+                r.by_k = kb.keep < kb.ties;
+                r.k = static_cast<int>(kb.above + kb.keep);
+                if (kb.above + kb.ties <= SP_CAP)
+                    n = gather<TL>(sm, ccnt = sm.ccnt[2], ck, rank, C, lcut, [](float) { return true; });
+            }
         }
     }
     if (n <= SP_CAP) {
@@ -1695,7 +2054,26 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
         }
     } else {
         bool summed = false;           // wsum holds the kept weights' sums
-        if (r.by_k || r.by_p) {
+        uint32_t kept = 0;             // counted: the border's ties that this CTA keeps,
+        uint32_t rx = 0xffffffffu;     // and the value of the certain draft, where it has that
+        if (counted) {
+            const uint32_t* hist = reinterpret_cast<const uint32_t*>(sm.lst);
+            kept = hist[kb.r];
+            if (r.by_k) {   // the first ones in index order
+                uint32_t before = 0;
+                for (uint32_t j = 0; j < rank; ++j) {
+                    uint32_t x;
+                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(sp_mapa(&hist[kb.r], j)) : "memory");
+                    before += x;
+                }
+                const uint32_t own = kept;
+                kept = min(own, kb.keep - min(kb.keep, before));
+                if (kept < own) {
+                    mask_ties<TL>(ck, tau, kept > 0 ? own_tie<TL>(sm, ck, tau, kept) : ck.begin - 1);
+                    __syncthreads();
+                }
+            }
+        } else if (r.by_k || r.by_p) {
             unsigned long long cut = 0;
             uint32_t dropped = 0;   // ties of the k-th token that top-k leaves behind
             if (r.by_k) {
@@ -1741,16 +2119,21 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
         if (r.x >= 0) {
             // the draft's weight, where it is kept, from the one CTA that holds it; a certain draft leaves the others
             const int i = r.x - ck.begin;
-            if (i >= 0 && i < ck.n && tid == 0) {
+            if (i >= 0 && i < ck.n) {
                 const float l = static_cast<float>(ck.buf[ck.mis + i]);
                 const double w = l >= tau ? sc.weight(l) : 0.0;
-                for (uint32_t j = 0; j < C; ++j) st_cluster_f64(&sm.wx, j, w);
-                if (!r.q) ck.mask(r.x);
+                if (counted && !r.q && w > 0.0) rx = keys.rank(l);
+                __syncthreads();
+                if (tid == 0) {
+                    for (uint32_t j = 0; j < C; ++j) st_cluster_f64(&sm.wx, j, w);
+                    if (!r.q) ck.mask(r.x);
+                }
             }
             if (summed) cluster_sync_warp0();
             else __syncthreads();
         }
-        if (!summed) segment_sums<TL>(sm.wsum, ck, rank, C, tau, sc);
+        if (counted) share_sums(sm.wsum, key_sum(sm, sc, keys, kb, kept, rx), rank, C);
+        else if (!summed) share_sums(sm.wsum, segment_part<TL>(ck, tau, sc), rank, C);
         if (r.x >= 0) wx = sm.wx;
         if (summed && wx > 0.0 && !r.q) {
             // the draft's segment without it
@@ -1773,12 +2156,47 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
             }
         }
         int tok = -1;
+        const double* sums = sm.wsum;
+        int nseg = static_cast<int>(C) * SP_WARPS, own_seg = static_cast<int>(rank) * SP_WARPS + warp;
+        double target = r.us * rest;
+        const float* q = nullptr;
         if (r.q) {
-            residual_sums<TL>(sm.rsum, ck, rank, C, tau, sc, r.q, S);
-            if (table_sum(sm.rsum, C, lane) > 0.0) tok = draw_token<TL>(sm.rsum, ck, rank, C, tau, sc, r.q, S, r.us);
-            else tok = draw_token<TL>(sm.wsum, ck, rank, C, tau, sc, nullptr, 0.0, r.us);
-        } else if (rest > 0.0) {
-            tok = draw_token<TL>(sm.wsum, ck, rank, C, tau, sc, nullptr, 0.0, r.us);
+            residual_sums<TL>(sm.rsum, ck, rank, C, tau, sc, r.q, S * 0x1p896);
+            const double left = table_sum(sm.rsum, C, lane);
+            if (left > 0.0) {
+                sums = sm.rsum;
+                target = r.us * left;
+                q = r.q;
+            }
+        }
+        if (counted && !q && rest > 0.0) {
+            // the table has sums per CTA only: the one that the draw falls to sums its segments
+            double base = 0.0, first = 0.0, end = 0.0;
+            int owner = -1;
+            for (uint32_t j = 0; j < C; ++j) {
+                const double x = warp_sum_f64(lane < SP_WARPS ? sm.wsum[j * SP_WARPS + lane] : 0.0);
+                if (x > 0.0 && (owner < 0 || end <= target)) {
+                    owner = static_cast<int>(j);
+                    first = base;
+                    end = base + x;
+                }
+                base += x;
+            }
+            own_seg = -2;   // (no segment of the others)
+            if (owner == static_cast<int>(rank)) {
+                double* own = sm.rsum + rank * SP_WARPS;
+                __syncthreads();
+                const double x = warp_sum_f64(segment_part<TL>(ck, tau, sc));
+                if (lane == 0) own[warp] = x;
+                __syncthreads();
+                sums = own;
+                nseg = SP_WARPS;
+                own_seg = warp;
+                target -= first;
+            }
+        }
+        if (q || rest > 0.0) {
+            if (own_seg >= 0) tok = draw_token<TL>(sums, nseg, own_seg, ck, tau, sc, q, S * 0x1p896, target);
         } else if (rank == 0 && warp == 0) {
             tok = r.x;   // the draft is the only token kept
         }

@@ -221,6 +221,46 @@ def test_random_numbers_outside_their_range_are_clamped(ms):
     assert torch.equal(a, b)
 
 
+def _around_zero(g, R, V):
+    """Rows whose kept sets end among very many small values: |l| far under the range between the maximum and the
+    last value with weight, ties among them, both signs of zero."""
+    z = g.standard_normal((R, V)) * np.logspace(-6, -1, R)[:, None]
+    z[:, ::7] = np.round(z[:, ::7] * 64) / 64
+    z[:, ::11] = -0.0
+    z[np.arange(R), g.integers(0, V, R)] = 30.0
+    z[:, ::5] = -g.exponential(size=z[:, ::5].shape) * 500
+    return z.astype(np.float32)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("par", [dict(top_p=0.6), dict(top_k=9000), dict(top_k=9000, top_p=0.9), dict(top_k=2500)],
+                         ids=["p", "k", "kp", "k2"])
+def test_borders_among_small_values(ms, par, dtype):
+    R, V = 12, 20003
+    g = np.random.default_rng(5)
+    t = torch.from_numpy(_around_zero(g, R, V)).to(DTYPES[dtype])
+    u = _uniform(g, R)
+    par = {k: np.full(R, v, np.int32 if k == "top_k" else np.float32) for k, v in par.items()}
+    par["temperature"] = np.repeat(np.array([50, 8, 500], np.float32), R // 3)
+    tok, probs = ms.sample(t.cuda(), dev(u), **_on(par), return_probs=True)
+    want, wp = sp.sample(t.float().numpy(), u, **par)
+    np.testing.assert_array_equal(host(tok), want)
+    _assert_probs(host(probs), wp)
+    # as verification: drafts among the small values, certain and with their distributions
+    B, K = R // 3, 2
+    z = t.view(B, K + 1, V)
+    zh = z.float().numpy()
+    d = g.integers(0, V, (B, K)).astype(np.int32)
+    uv = _uniform(g, (B, K + 1)) * np.float32(1e-3)
+    pv = {k: v[:: 3].copy() for k, v in par.items()}
+    q = np.full((B, K, V), 1.0 / V, np.float32)
+    for qq in (None, q):
+        cm, n = ms.verify_sample(z.cuda(), dev(d), dev(uv), draft_probs=None if qq is None else dev(qq), **_on(pv))
+        wcm, wn = sp.verify(zh, d, uv, qq, **pv)
+        np.testing.assert_array_equal(host(cm), wcm)
+        np.testing.assert_array_equal(host(n), wn)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_sample_from_any_element_offset(ms, dtype):
     """Rows and outputs that start at any element, filters that take every path."""
