@@ -604,46 +604,59 @@ __device__ uint32_t gather(SampleSmem& sm, uint32_t* ccnt, const SpChunk<TL>& ck
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
-    uint32_t n = 0;
+    constexpr uint32_t kRoom = SP_CAP / SP_WARPS;
     const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(floor);
-    for (int q = q0 + lane; q < q1; q += 32) {
-        const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[q];
-        if (!SpElem<TL>::any_ge(raw, tb)) continue;
-        float v[VEC];
-        SpElem<TL>::unpack(raw, v);
+    // this warp's entries from loc[from] on, as far as `room`; returns their number
+    auto list = [&](uint32_t from, uint32_t room) {
+        uint32_t n = 0;
+        for (int v0 = q0; v0 < q1; v0 += 32) {
+            const uint4 raw = ck.raw_to(v0 + lane, q1);
+            if (!__any_sync(0xffffffffu, SpElem<TL>::any_ge(raw, tb))) continue;
+            uint32_t mask = 0, all;
+            float v[VEC];
+            SpElem<TL>::unpack(raw, v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) n += v[e] >= floor && keep(v[e]) ? 1u : 0u;
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
+            for (int e = 0; e < VEC; ++e) mask |= (v[e] >= floor && keep(v[e]) ? 1u : 0u) << e;
+            uint32_t w = n + lanes_before(__popc(mask), lane, all);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (mask & (1u << e)) {
+                    if (w < room) sm.loc[from + w] = composite(v[e], ck.index(v0 + lane, e));
+                    ++w;
+                }
+            n += all;
+        }
+        return n;
+    };
+    // into a part of loc for each warp, then together; a second pass where one has more than that
+    const uint32_t n = list(warp * kRoom, kRoom);
     if (lane == 0) sm.wcnt[warp] = n;
     __syncthreads();
-    uint32_t at = 0, tot = 0;
+    uint32_t at = 0, tot = 0, most = 0;
 #pragma unroll
     for (int w = 0; w < SP_WARPS; ++w) {
         const uint32_t x = sm.wcnt[w];
         if (w < warp) at += x;
         tot += x;
+        most = max(most, x);
     }
     if (tid < static_cast<int>(C)) st_cluster_s32(&ccnt[rank], tid, static_cast<int>(tot));
     if (start) {
         *start = at;
         *count = n;
     }
-    if (tot <= SP_CAP && n > 0) {
-        for (int v0 = q0; v0 < q1; v0 += 32) {
-            const uint4 raw = ck.raw_to(v0 + lane, q1);
-            if (!__any_sync(0xffffffffu, SpElem<TL>::any_ge(raw, tb))) continue;
-            uint32_t mask = 0;
-            float v[VEC];
-            SpElem<TL>::unpack(raw, v);
+    if (tot <= SP_CAP) {
+        if (most <= kRoom) {
+            unsigned long long k[kRoom / 32];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) mask |= (v[e] >= floor && keep(v[e]) ? 1u : 0u) << e;
-            uint32_t all;
-            uint32_t w = at + lanes_before(__popc(mask), lane, all);
+            for (uint32_t i = 0; i < kRoom / 32; ++i)
+                if (lane + 32 * i < n) k[i] = sm.loc[warp * kRoom + lane + 32 * i];
+            __syncthreads();
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (mask & (1u << e)) sm.loc[w++] = composite(v[e], ck.index(v0 + lane, e));
-            at += all;
+            for (uint32_t i = 0; i < kRoom / 32; ++i)
+                if (lane + 32 * i < n) sm.loc[at + lane + 32 * i] = k[i];
+        } else {
+            list(at, n);
         }
     }
     cluster_sync_warp0();
