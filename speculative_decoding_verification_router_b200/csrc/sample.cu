@@ -11,14 +11,32 @@
 // A decision (is the prefix long enough, does the cumulative sum pass u S)
 // must not depend on rounding: with 10^5 tokens of similar weight the
 // borders of the cumulative sum are 10^-5 apart, so an error of 10^-7 (fp32)
-// would move one draw in a hundred.  Weights are therefore computed to ~10^-13
-// and summed in fp64 in a fixed order; sums that pass through integer
-// histograms are fixed point (2^-45), so that their order cannot matter.
+// would move one draw in a hundred.  Weights are therefore computed in fp64 to
+// about 2e-13 and summed in a fixed order; histograms hold counts, whose order
+// cannot matter, and sums of a count times a weight.
 //
 // One thread-block cluster per row: each CTA copies its part of the row into
 // shared memory once, and every later pass (maximum, selection, sums, the
 // draw) reads it from there; partial results cross the cluster through
-// distributed shared memory.
+// distributed shared memory.  A row takes one of three ways:
+//  - few tokens kept (top-k of up to SP_CAP, a top-p or min-p set as small):
+//    they are listed, in index order, and one CTA sorts, cuts and draws;
+//  - a bf16 row that keeps more: every value of the row is counted (a bf16 row
+//    has few), which gives its borders exactly by one scan;
+//  - other rows that keep more: counts over 1024 intervals of the logit bracket
+//    the border, the tokens of the bracket are listed and refined by their bits.
+// A row without filters needs the sums alone.
+//
+// What bounds it: one row's time is the chain of cluster barriers (0.25 us each
+// at 1.9 GHz) and block scans; many rows are bound by instructions, 21 per
+// element and fp64 pass, 11 of them fp64 at two issue cycles.  Memory is not the
+// bound: the row is read once.  Measured at V = 129,280 (replayed in a graph):
+//   1 bf16 row, all filters                       7.7 us
+//   32 fp32 rows, top-p (3 of them wide)           57 us
+//   64 bf16 rows, temperature, probs written       36 us  (1.4 TB/s)
+//   512 bf16 rows, filters of every kind          132 us  (1.0 TB/s)
+//   verification of 32 x 4 bf16 rows, top-p        91 us
+//   the same by temperature with draft probs       63 us  (0.8 TB/s)
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -1152,6 +1170,11 @@ __device__ void draw_from_list(SampleSmem& sm, int n, int ksh, float lcut, const
 // around zero.  One pass counts each (the values of magnitude at most m0 as one,
 // their weights summed apart); counts times weights are then exact sums in the
 // order of the selection, and the borders of top-k and top-p follow by a scan.
+// The pass is bound by shared-memory atomics (35 cycles per 32 elements and
+// quarter of an SM, as much as an fp64 pass), so it replaces the later passes of
+// rows that keep many tokens and not the first of every row: by intervals and
+// refinement the 512 mixed rows take 154 us instead of 132, the 32 x 4 rows of
+// a top-p verification 101 instead of 91.
 constexpr int SP_KEYS = 4096;
 static_assert(SP_KEYS * sizeof(uint32_t) <= sizeof(SampleSmem::lst), "the counts share the candidates' memory");
 constexpr int SP_KPT = SP_KEYS / SP_THREADS;
@@ -1658,12 +1681,26 @@ __device__ uint32_t refine(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale&
     }
 }
 
+// A bit per element of vector i that equals tau.
+template <typename TL>
+__device__ __forceinline__ uint32_t tie_mask(const SpChunk<TL>& ck, int i, float tau) {
+    constexpr int VEC = SpElem<TL>::VEC;
+    const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[i];
+    uint32_t mask = 0;
+    if (SpElem<TL>::any_eq(raw, tau)) {
+        float v[VEC];
+        SpElem<TL>::unpack(raw, v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) mask |= (v[e] == tau ? 1u : 0u) << e;
+    }
+    return mask;
+}
+
 // Index of the keep-th token with logit tau, in index order (two cluster
 // barriers).
 template <typename TL>
 __device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, const SpWindow& win, float tau,
                          uint32_t keep) {
-    constexpr int VEC = SpElem<TL>::VEC;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
@@ -1673,15 +1710,7 @@ __device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, u
     auto ties_at = [&](int i) -> uint32_t {   // a bit per element of entry or vector i
         if (i >= last) return 0;
         if (win.listed) return composite_value(sm.loc[i]) == tau ? 1u : 0u;
-        const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[i];
-        uint32_t mask = 0;
-        if (SpElem<TL>::any_eq(raw, tau)) {
-            float v[VEC];
-            SpElem<TL>::unpack(raw, v);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) mask |= (v[e] == tau ? 1u : 0u) << e;
-        }
-        return mask;
+        return tie_mask<TL>(ck, i, tau);
     };
     uint32_t n = 0;
     for (int i = first + lane; i < last; i += 32) n += __popc(ties_at(i));
@@ -1720,22 +1749,10 @@ __device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, u
 // Index of the keep-th of this CTA's elements equal to tau.
 template <typename TL>
 __device__ int own_tie(SampleSmem& sm, const SpChunk<TL>& ck, float tau, uint32_t keep) {
-    constexpr int VEC = SpElem<TL>::VEC;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
-    auto ties_at = [&](int i) -> uint32_t {
-        if (i >= q1) return 0;
-        const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[i];
-        uint32_t mask = 0;
-        if (SpElem<TL>::any_eq(raw, tau)) {
-            float v[VEC];
-            SpElem<TL>::unpack(raw, v);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) mask |= (v[e] == tau ? 1u : 0u) << e;
-        }
-        return mask;
-    };
+    auto ties_at = [&](int i) { return i < q1 ? tie_mask<TL>(ck, i, tau) : 0u; };
     uint32_t n = 0;
     for (int i = q0 + lane; i < q1; i += 32) n += __popc(ties_at(i));
     n = __reduce_add_sync(0xffffffffu, n);
@@ -1879,6 +1896,11 @@ __device__ void write_probs(float* out, const SpChunk<TL>& ck, float tau, const 
     }
 }
 
+// One cluster per row.  512 threads and half of an SM's shared memory per CTA:
+// two of them overlap one row's barriers with the other's passes (CTAs of 256
+// threads took 51 us against 45 then, on 64 rows with probs).  Copying the part
+// once beats re-reading it from L2 in every pass: clusters of 1 or 2 that do so
+// took 315 and 206 us on the 512 mixed rows, against 148 then.
 template <typename TL, bool VERIFY>
 __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(const SampleArgs a) {
     constexpr int VEC = SpElem<TL>::VEC;
@@ -2262,7 +2284,9 @@ static ms_status sample_launch_t(const SampleArgs& a, cudaStream_t s) {
 
 static ms_status sample_launch(SampleArgs a, ms_dtype dt, bool verify, cudaStream_t s) {
     // The smallest cluster whose parts leave room for two CTAs per SM, then
-    // wider while all rows still run at once.
+    // wider while all rows still run at once.  At V = 129,280 one bf16 row takes
+    // 8.5 us on 4 CTAs and 7.7 on 8, 512 rows 132 us on 4 and 193 on 8; 42 fp32 rows
+    // of 32,003 take 35 us on 2, 24 on 4 and 29 on 8.
     const int eb = dt == MS_BF16 ? 2 : 4;
     int C = 1;
     while (C < SP_MAXC && static_cast<long>(a.V) * eb > 66L * 1024 * C) C *= 2;
