@@ -179,6 +179,7 @@ template <>
 struct SpElem<float> {
     static constexpr int VEC = 4;
     static constexpr int KSH = 0;
+    static constexpr double OCTAVES = 20.0;
     using Bound = float;   // a threshold as the comparisons below want it
     static __device__ __forceinline__ Bound bound(float t) { return t; }
     static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[4]) {
@@ -215,6 +216,7 @@ template <>
 struct SpElem<__nv_bfloat16> {
     static constexpr int VEC = 8;
     static constexpr int KSH = 16;   // the low half of a widened bf16 carries nothing
+    static constexpr double OCTAVES = 16.0;
     using Bound = __nv_bfloat162;
     // l >= t for bf16 l holds exactly where l >= t rounded up to bf16
     static __device__ __forceinline__ Bound bound(float t) {
@@ -277,7 +279,7 @@ struct SampleSmem {
     double wx;
     unsigned long long lst[SP_CAP];           // leader: the row's candidates in index order
     unsigned long long loc[SP_CAP];           // this CTA's candidates; leader, later: scratch for sorting
-    uint32_t cnt[SP_BINS + 31];               // counts by interval; the last interval's in 32 parts, one per lane
+    uint32_t cnt[SP_BINS];                    // counts by interval
     float cmax[SP_MAXC], cmin[SP_MAXC];       // every CTA's maximum, and the least of its threads' maxima
     uint32_t ccnt[4][SP_MAXC];                // every CTA's count, of each of up to four gathers
     uint32_t tie[SP_MAXC];
@@ -399,10 +401,11 @@ struct SpBins {
     }
 };
 
-// First round: intervals of the logit itself over the 24 binary orders of
+// First round: intervals of the logit itself over the OCTAVES binary orders of
 // magnitude below the largest weight, or down to `lo` where that is nearer.
+template <typename TL>
 __device__ __forceinline__ SpBins first_bins(const SpScale& sc, float lo) {
-    const float width = fminf(sc.m - lo, static_cast<float>(24.0 / sc.c));
+    const float width = fminf(sc.m - lo, static_cast<float>(SpElem<TL>::OCTAVES / sc.c));
     return SpBins{sc.m, width > 0.f && width < 1e30f ? static_cast<float>(SP_BINS - 1) / width : 0.f};
 }
 
@@ -451,23 +454,16 @@ __device__ __forceinline__ void pull_counts(SampleSmem& sm, uint32_t C, uint32_t
         }
 }
 
-// Counts a vector's elements at or above lo by interval.  The last interval
-// takes the bulk of a peaked row: each lane counts it in a word of its own.
+// Counts a vector's elements at or above lo by interval, but for the last one:
+// that takes the bulk of a peaked row, where a border seldom lies.
 template <typename TL>
-__device__ __forceinline__ void count_vector(SampleSmem& sm, const uint4& raw, float lo, const SpBins& bins, uint32_t most) {
+__device__ __forceinline__ void count_vector(SampleSmem& sm, const uint4& raw, float lo, const SpBins& bins) {
     float v[SpElem<TL>::VEC];
     SpElem<TL>::unpack(raw, v);
 #pragma unroll
     for (int e = 0; e < SpElem<TL>::VEC; ++e) {
-        const uint32_t b = min(bins.raw(v[e]), most);
-        if (v[e] >= lo) atomicAdd(&sm.cnt[b], 1u);
-    }
-}
-// The last interval's parts as one count (between block barriers).
-__device__ __forceinline__ void join_last(SampleSmem& sm) {
-    if (threadIdx.x < 32) {
-        const uint32_t n = __reduce_add_sync(0xffffffffu, sm.cnt[SP_BINS - 1 + threadIdx.x]);
-        if (threadIdx.x == 0) sm.cnt[SP_BINS - 1] = n;
+        const uint32_t b = bins.raw(v[e]);
+        if (v[e] >= lo && b < SP_BINS - 1) atomicAdd(&sm.cnt[b], 1u);
     }
 }
 
@@ -478,24 +474,23 @@ __device__ __forceinline__ void join_last(SampleSmem& sm) {
 // sums from both sides.  Clears nothing: sm.cnt is zero in every CTA when called.
 struct SpNucleus {
     double S;
-    uint32_t b0, b1, n;   // n: tokens down to b1
+    uint32_t b0, b1, n;   // n: tokens down to b1, at most
 };
 template <typename TL>
 __device__ SpNucleus nucleus(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
-                             float lo, double p, double minus) {
+                             int V, float lo, double p, double minus) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const SpBins bins = first_bins(sc, lo);
+    const SpBins bins = first_bins<TL>(sc, lo);
     int q0, q1;
     warp_segment(ck.nvec, warp, q0, q1);
     double s0 = 0.0, s1 = 0.0;
     const typename SpElem<TL>::Bound tb = SpElem<TL>::bound(lo);
     for (int v0 = q0; v0 < q1; v0 += 32) {
         const uint4 raw = ck.raw_to(v0 + lane, q1);
-        count_vector<TL>(sm, raw, lo, bins, SP_BINS - 1 + lane);
+        count_vector<TL>(sm, raw, lo, bins);
         add_weights<TL>(raw, lo, tb, sc, s0, s1);
     }
     __syncthreads();
-    join_last(sm);
     share_sums(sm.wsum, s0 + s1, rank, C);
     SpNucleus r;
     r.S = table_sum(sm.wsum, C, lane) - minus;
@@ -558,25 +553,23 @@ __device__ SpNucleus nucleus(SampleSmem& sm, const SpChunk<TL>& ck, const SpScal
     for (int j = 0; j < SP_BPT; ++j)
         if (r.b1 == static_cast<uint32_t>(SP_BPT * tid + j)) sm.nn = run[j];
     __syncthreads();
-    r.n = sm.nn;
+    r.n = r.b1 < SP_BINS - 1 ? sm.nn : V;
     return r;
 }
 
 // Top-k over the elements at or above lo, first step: the interval that holds
-// the k-th (the last one where there are fewer), and the tokens above it.
+// the k-th (the last one where the others hold fewer), and the tokens above it.
 // Clears nothing: sm.cnt is zero in every CTA when called.
 struct SpKth {
-    uint32_t b, above, cnt;
+    uint32_t b, above;
 };
 template <typename TL>
 __device__ SpKth kth_interval(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t C, float lo,
                               uint32_t k) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const SpBins bins = first_bins(sc, lo);
+    const SpBins bins = first_bins<TL>(sc, lo);
     for (int q = tid; q < ck.nvec; q += SP_THREADS)
-        count_vector<TL>(sm, reinterpret_cast<const uint4*>(ck.buf)[q], lo, bins, SP_BINS - 1 + lane);
-    __syncthreads();
-    join_last(sm);
+        count_vector<TL>(sm, reinterpret_cast<const uint4*>(ck.buf)[q], lo, bins);
     cluster_sync_warp0();
     uint32_t n[SP_BPT], own = 0;
     pull_counts(sm, C, n);
@@ -590,18 +583,17 @@ __device__ SpKth kth_interval(SampleSmem& sm, const SpChunk<TL>& ck, const SpSca
         if (w < warp) ex += sm.wcnt[w];
         tot += sm.wcnt[w];
     }
-    k = min(k, tot);
+    if (tot < k) return SpKth{SP_BINS - 1, tot};
 #pragma unroll
     for (int j = 0; j < SP_BPT; ++j) {
         if (ex < k && ex + n[j] >= k) {
             sm.nb0 = SP_BPT * tid + j;
             sm.nb1 = ex;
-            sm.nn = n[j];
         }
         ex += n[j];
     }
     __syncthreads();
-    return SpKth{sm.nb0, sm.nb1, sm.nn};
+    return SpKth{sm.nb0, sm.nb1};
 }
 
 // The logit that a key stands for.
@@ -1520,7 +1512,8 @@ __device__ int draw_token(const double* sums, int nseg, int own_seg, const SpChu
 // where one CTA has too many, found by passes over the row.
 struct SpWindow {
     bool listed;
-    uint32_t mine, start, count;   // this CTA's entries; this warp's range of them
+    uint32_t all, mine;            // the cluster's entries, this CTA's;
+    uint32_t start, count;         // this warp's range of them
     float bot, top;                // bounds of the intervals' logits
     SpBins bins;
     uint32_t b0, b1;
@@ -1555,7 +1548,7 @@ __device__ SpWindow make_window(SampleSmem& sm, uint32_t* ccnt, const SpChunk<TL
     w.b1 = b1;
     w.bot = bins.lower(b1, lo);
     w.top = bins.upper(b0);
-    gather<TL>(sm, ccnt, ck, rank, C, w.bot, [&](float l) { const uint32_t b = bins.of(l); return b >= b0 && b <= b1; },
+    w.all = gather<TL>(sm, ccnt, ck, rank, C, w.bot, [&](float l) { const uint32_t b = bins.of(l); return b >= b0 && b <= b1; },
                &w.start, &w.count);
     uint32_t most = 0;
     for (uint32_t r = 0; r < C; ++r) most = max(most, ccnt[r]);
@@ -1779,7 +1772,7 @@ __device__ int own_tie(SampleSmem& sm, const SpChunk<TL>& ck, float tau, uint32_
 
 // The count table of every CTA to zero (one cluster barrier).
 __device__ void clear_counts(SampleSmem& sm) {
-    for (int i = threadIdx.x; i < SP_BINS + 31; i += SP_THREADS) sm.cnt[i] = 0;
+    for (int i = threadIdx.x; i < SP_BINS; i += SP_THREADS) sm.cnt[i] = 0;
     cluster_sync_warp0();
 }
 
@@ -1910,7 +1903,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
     const int row = blockIdx.x / a.cluster;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < 16) sm.tab[tid] = __hiloint2double(__double2hiint(exp2(tid / 16.0)) - (tid << 16), __double2loint(exp2(tid / 16.0)));
-    for (int i = tid; i < SP_BINS + 31; i += SP_THREADS) sm.cnt[i] = 0;
+    for (int i = tid; i < SP_BINS; i += SP_THREADS) sm.cnt[i] = 0;
     cluster_arrive();   // waited for before the first store to another CTA: all have started then
     grid_dep_wait();
     grid_dep_launch();
@@ -2030,10 +2023,10 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
     }
     SpNucleus nu{};
     if (n > SP_CAP && r.by_p && !r.by_k) {
-        nu = nucleus<TL>(sm, ck, sc, rank, C, lcut, r.p, 0.0);
+        nu = nucleus<TL>(sm, ck, sc, rank, C, a.V, lcut, r.p, 0.0);
         S_all = nu.S;
         if (nu.n <= SP_CAP) {
-            const SpBins bins = first_bins(sc, lcut);
+            const SpBins bins = first_bins<TL>(sc, lcut);
             n = gather<TL>(sm, ccnt = sm.ccnt[1], ck, rank, C, bins.lower(nu.b1, lcut), [&](float l) { return bins.of(l) <= nu.b1; });
         }
     }
@@ -2042,7 +2035,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
     SpBorder kb{};
     if constexpr (SpElem<TL>::KSH == 16) {
         if (n > SP_CAP && (r.by_k || r.by_p)) {
-            const float lo = r.by_k ? lcut : first_bins(sc, lcut).lower(nu.b1, lcut);
+            const float lo = r.by_k ? lcut : first_bins<TL>(sc, lcut).lower(nu.b1, lcut);
             keys = make_keys(m, __bfloat162float(__float2bfloat16_ru(lo)));
             // (not with a cut or a certain draft among the collapsed values)
             bool can = !keys.mixed(keys.n - 1);
@@ -2114,25 +2107,27 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
             if (r.by_k) {
                 clear_counts(sm);
                 const SpKth kt = kth_interval<TL>(sm, ck, sc, C, lcut, static_cast<uint32_t>(r.k));
-                const SpBins bins = first_bins(sc, lcut);
-                const uint32_t left = min(static_cast<uint32_t>(r.k) - min(kt.above, static_cast<uint32_t>(r.k) - 1), kt.cnt);
+                const SpBins bins = first_bins<TL>(sc, lcut);
                 const SpWindow win = make_window<TL>(sm, sm.ccnt[2], ck, rank, C, lcut, bins, kt.b, kt.b);
-                uint32_t keep, ties;
-                const float v = key_logit<TL>(refine<TL>(sm, ck, sc, rank, C, win, true, static_cast<double>(kt.above),
-                                                         static_cast<double>(kt.above) + static_cast<double>(left), keep, ties));
-                dropped = ties - keep;
-                cut = composite(v, dropped ? tie_index<TL>(sm, ck, rank, C, win, v, keep) : -1);
+                cut = composite(lcut, -1);   // (fewer than k)
+                if (win.all) {
+                    uint32_t keep, ties;
+                    const float v = key_logit<TL>(
+                        refine<TL>(sm, ck, sc, rank, C, win, true, static_cast<double>(kt.above), static_cast<double>(r.k), keep, ties));
+                    dropped = ties - keep;
+                    cut = composite(v, dropped ? tie_index<TL>(sm, ck, rank, C, win, v, keep) : -1);
+                }
             }
             if (r.by_p) {
                 const float kth = r.by_k ? composite_value(cut) : lcut;
                 if (r.by_k) {
                     if (!dropped) cluster_sync_warp0();   // the other CTAs have read refine()'s counts (tie_index() waits too)
                     clear_counts(sm);
-                    nu = nucleus<TL>(sm, ck, sc, rank, C, kth, r.p, static_cast<double>(dropped) * sc.weight(kth));
+                    nu = nucleus<TL>(sm, ck, sc, rank, C, a.V, kth, r.p, static_cast<double>(dropped) * sc.weight(kth));
                 }
                 // the border lies in intervals b0..b1: the sum above them, then token by token
                 const double target = fmax(r.p * nu.S, 1e-9);
-                const SpBins bins = first_bins(sc, kth);
+                const SpBins bins = first_bins<TL>(sc, kth);
                 const double mine_above = above_part<TL>(ck, kth, bins, nu.b0, sc);
                 share_sums(sm.rsum, mine_above, rank, C);
                 const double A = table_sum(sm.rsum, C, lane);
