@@ -2284,7 +2284,7 @@ static ms_status sample_launch(SampleArgs a, ms_dtype dt, bool verify, cudaStrea
     // of 32,003 take 35 us on 2, 24 on 4 and 29 on 8.
     const int eb = dt == MS_BF16 ? 2 : 4;
     int C = 1;
-    while (C < SP_MAXC && static_cast<long>(a.V) * eb > 66L * 1024 * C) C *= 2;
+    while (C < SP_MAXC && (static_cast<long>(a.V) * eb > 66L * 1024 * C || a.V > SP_MAX_CHUNK * C)) C *= 2;
     while (C < SP_MAXC && a.V > 1024 * C && 2L * C * a.rows <= 2L * num_sms()) C *= 2;
     a.cluster = C;
     a.chunk = ((a.V + C - 1) / C + 7) / 8 * 8;

@@ -138,6 +138,28 @@ def test_sample_largest_vocabulary(ms, V):
     np.testing.assert_array_equal(host(tok), sp.sample(z.numpy(), u, **par)[0])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [16896, 16897, 32768, 32769, 33792, 33793, 65537, 66310, 67585, 131073, 135169])
+def test_vocabularies_around_the_parts_of_a_cluster(ms, V, dtype):
+    """Full batches (clusters no wider than the rows need) on both sides of the sizes at which a row takes another CTA."""
+    R = 160
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = (2 * torch.randn(R, V, generator=g, device="cuda")).to(DTYPES[dtype])
+    u = torch.rand(R, generator=g, device="cuda")
+    par = dict(temperature=torch.full((R,), 0.9, device="cuda"),
+               top_p=torch.tensor([1.0, 0.9, 0.5, 1.0] * (R // 4), device="cuda"),
+               top_k=torch.tensor([0, 0, 0, 50] * (R // 4), dtype=torch.int32, device="cuda"))
+    tok, probs = ms.sample(z, u, **par, return_probs=True)
+    at = [0, 1, 2, 3, R - 4, R - 3, R - 2, R - 1]
+    want, wp = sp.sample(host(z[at].float()), host(u[at]), **{k: host(v[at]) for k, v in par.items()})
+    np.testing.assert_array_equal(host(tok[at]), want)
+    _assert_probs(host(probs[at]), wp)
+    for r in range(4, R - 4, 13):   # alone, a row takes a wider cluster
+        t, p = ms.sample(z[r:r + 1], u[r:r + 1], **{k: v[r:r + 1] for k, v in par.items()}, return_probs=True)
+        assert torch.equal(t, tok[r:r + 1])
+        assert bool(((p - probs[r:r + 1]).abs() <= 2.0 ** -23 * p).all())   # both round sums that agree to 1e-15
+
+
 def test_equal_weights_are_split_exactly(ms):
     # the border cases that rounding would decide: 2n equal weights, top_p 0.5 keeps n, u = i / 2n draws token i
     for n in (4, 512, 4096):
