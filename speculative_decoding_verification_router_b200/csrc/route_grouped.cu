@@ -21,10 +21,12 @@
 // What bounds it: the sorting networks (minimum and maximum at half the rate of
 // an add) and, in a launch of a few waves, the tail of its last blocks; memory
 // asks for a tenth of the time.  Measured (replayed in a graph):
-//   128 tokens, 64 experts, fp32, bias               4.5 us
-//   36,992 tokens, 64 experts, fp32, 8 groups       15.0 us  (0.75 TB/s)
-//   8,191 tokens, 256 experts, fp32, bias, groups   16.7 us  (0.53 TB/s)
-//   36,992 tokens, 256 experts, bf16, bias, groups  30.1 us  (0.71 TB/s)
+//   128 tokens, 64 experts, fp32, bias               4.4 us
+//   36,992 tokens, 64 experts, fp32, 8 groups       14.2 us  (0.79 TB/s)
+//   8,191 tokens, 256 experts, fp32, bias, groups   15.7 us  (0.57 TB/s)
+//   36,992 tokens, 256 experts, bf16, bias, groups  28.3 us  (0.75 TB/s)
+// (The parameters are __grid_constant__: the exact form takes them by reference,
+// and a copy of them in every thread's local memory costs 6 % of that.)
 #include <limits.h>
 #include <math.h>
 
@@ -210,9 +212,9 @@ __device__ __noinline__ void route_token_exact(const RouteGroupedArgs& a, int t,
 
 // Any shape, in the exact form: one warp per token.  It is for the shapes that
 // the fast form cannot take: 36,992 tokens of 64 and of 256 experts took 62 and
-// 121 us by it, 15 and 30 by the other.
+// 121 us by it, 14 and 28 by the other.
 template <typename TL>
-__global__ void __launch_bounds__(RG_WARPS * 32) route_grouped_kernel(const RouteGroupedArgs a) {
+__global__ void __launch_bounds__(RG_WARPS * 32) route_grouped_kernel(const __grid_constant__ RouteGroupedArgs a) {
     __shared__ double sel[RG_WARPS][RG_MAXE];
     __shared__ double score[RG_WARPS][RG_MAXE];
     grid_dep_wait();
@@ -291,11 +293,12 @@ static_assert(sizeof(RouteClose) <= RG_MAXE / 4 * sizeof(double), "four of them 
 // Eight lanes per token, four tokens per warp: a group is one or more whole
 // lanes, and a list of 8 keys per lane is sorted in registers.  Three blocks per
 // SM at 256 experts (80 registers): with two 40, with four (64 registers) 41 us
-// instead of 36 when measured.  Lane l holds the P = E / 8 neighbours from l P on, as
+// against 36 then; four at 64 experts: 14.2 us, with five 14.6.  Lane l holds the P = E / 8 neighbours from l P on, as
 // NL lists of 8.  E a multiple of 8, at most 8 groups (a power of two), k <= 8.
 // FULL: P = 8 NL, aligned for vector loads.
 template <typename TL, int NL, bool REST, bool FULL>
-__global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4) route_grouped_fast_kernel(const RouteGroupedArgs a) {
+__global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
+    route_grouped_fast_kernel(const __grid_constant__ RouteGroupedArgs a) {
     __shared__ double sel[RG_WARPS][RG_MAXE];
     __shared__ double score[RG_WARPS][RG_MAXE];
     grid_dep_wait();
