@@ -34,7 +34,7 @@
 //   1 bf16 row, all filters                       7.7 us
 //   32 fp32 rows, top-p (3 of them wide)           57 us
 //   64 bf16 rows, temperature, probs written       36 us  (1.4 TB/s)
-//   512 bf16 rows, filters of every kind          132 us  (1.0 TB/s)
+//   512 bf16 rows, filters of every kind          131 us  (1.0 TB/s)
 //   verification of 32 x 4 bf16 rows, top-p        91 us
 //   the same by temperature with draft probs       63 us  (0.8 TB/s)
 #include <float.h>
@@ -677,36 +677,34 @@ __device__ uint32_t gather(SampleSmem& sm, uint32_t* ccnt, const SpChunk<TL>& ck
 
 // A lower bound of the k-th largest of the elements at or above lo: the k-th
 // largest of the threads' maxima (each of k threads holds an element at least
-// that large), to within one of SP_BINS intervals between low and high, the
+// that large), to within one of SP_THREADS intervals between low and high, the
 // least and the largest of those maxima.  lo where fewer than k threads hold an
 // element that large.
 __device__ float kth_bound(SampleSmem& sm, uint32_t C, float lo, float low, float high, float mine, uint32_t k) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     low = fmaxf(low, lo);
     const float width = high - low;
-    const SpBins bins{high, width > 0.f && width < 1e30f ? static_cast<float>(SP_BINS - 1) / width : 0.f};
-    if (mine >= lo) atomicAdd(&sm.cnt[bins.of(mine)], 1u);   // the table is clear when called
+    const SpBins bins{high, width > 0.f && width < 1e30f ? static_cast<float>(SP_THREADS - 1) / width : 0.f};
+    if (mine >= lo) atomicAdd(&sm.cnt[min(bins.raw(mine), SP_THREADS - 1u)], 1u);   // the table is clear when called
     cluster_sync_warp0();
-    uint32_t n[SP_BPT], own = 0;
-    pull_counts(sm, C, n);
-    if (tid == 0) sm.last = SP_BINS;
-#pragma unroll
-    for (int j = 0; j < SP_BPT; ++j) own += n[j];
-    const uint32_t inc = warp_scan(own, lane);
-    if (lane == 31) sm.wcnt[warp] = inc;
-    __syncthreads();
-    uint32_t ex = inc - own;
-    for (int w = 0; w < warp; ++w) ex += sm.wcnt[w];
-#pragma unroll
-    for (int j = 0; j < SP_BPT; ++j) {
-        if (ex < k && ex + n[j] >= k) sm.last = SP_BPT * tid + j;
-        ex += n[j];
+    uint32_t n = 0;
+#pragma unroll 8
+    for (uint32_t r = 0; r < C; ++r) {
+        uint32_t x;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(sp_mapa(&sm.cnt[tid], r)) : "memory");
+        n += x;
     }
+    if (tid == 0) sm.last = SP_THREADS;
+    uint32_t in = warp_scan(n, lane);
+    if (lane == 31) sm.wcnt[warp] = in;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) in += sm.wcnt[w];
+    if (in - n < k && in >= k) sm.last = tid;
     __syncthreads();
     const int b = sm.last;
     __syncthreads();   // wcnt and last are free again
-    if (b == SP_BINS - 1 && bins.s > 0.f) return low;   // all of the maxima
-    return bins.lower(b, lo);
+    if (b < SP_THREADS - 1 || !(bins.s > 0.f)) return bins.lower(b, lo);
+    return b < SP_THREADS ? low : lo;   // all of the maxima, or too few
 }
 
 // ---------------------------------------------------------------- the draw from a list (leader)
@@ -1165,7 +1163,7 @@ __device__ void draw_from_list(SampleSmem& sm, int n, int ksh, float lcut, const
 // The pass is bound by shared-memory atomics (35 cycles per 32 elements and
 // quarter of an SM, as much as an fp64 pass), so it replaces the later passes of
 // rows that keep many tokens and not the first of every row: by intervals and
-// refinement the 512 mixed rows take 154 us instead of 132, the 32 x 4 rows of
+// refinement the 512 mixed rows take 154 us instead of 131, the 32 x 4 rows of
 // a top-p verification 101 instead of 91.
 constexpr int SP_KEYS = 4096;
 static_assert(SP_KEYS * sizeof(uint32_t) <= sizeof(SampleSmem::lst), "the counts share the candidates' memory");
@@ -2280,7 +2278,7 @@ static ms_status sample_launch_t(const SampleArgs& a, cudaStream_t s) {
 static ms_status sample_launch(SampleArgs a, ms_dtype dt, bool verify, cudaStream_t s) {
     // The smallest cluster whose parts leave room for two CTAs per SM, then
     // wider while all rows still run at once.  At V = 129,280 one bf16 row takes
-    // 8.5 us on 4 CTAs and 7.7 on 8, 512 rows 132 us on 4 and 193 on 8; 42 fp32 rows
+    // 8.5 us on 4 CTAs and 7.7 on 8, 512 rows 131 us on 4 and 193 on 8; 42 fp32 rows
     // of 32,003 take 35 us on 2, 24 on 4 and 29 on 8.
     const int eb = dt == MS_BF16 ? 2 : 4;
     int C = 1;
