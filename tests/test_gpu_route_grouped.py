@@ -58,6 +58,19 @@ def test_route_grouped_matches_the_oracle(ms, E, groups, score, dtype):
                    renormalize=renorm, scale=2.5)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(9, 3), (96, 3), (90, 5), (150, 6), (96, 12), (48, 16), (124, 31), (200, 25), (32, 32)])
+def test_group_counts_that_are_no_power_of_two(ms, E, groups, score):
+    g = np.random.default_rng(E)
+    z = _logits(g, 41, E)
+    for tg in sorted({1, 2, groups - 1}):
+        for top in (1, 2):
+            k = min(32, tg * (E // groups))
+            bias = (0.1 * g.standard_normal(E)).astype(np.float32) if top == 1 else None
+            _check(ms, z, k, "f32", bias=bias, score=score, n_groups=groups, topk_groups=tg, group_top=top,
+                   renormalize=True, scale=1.5)
+
+
 @pytest.mark.parametrize("T", [1, 7, 9, 36992])
 def test_route_grouped_token_counts(ms, T):
     g = np.random.default_rng(T)

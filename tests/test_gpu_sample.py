@@ -235,6 +235,24 @@ def test_extreme_temperatures(ms):
                 _assert_probs(host(probs), wp)
 
 
+def test_parameters_that_leave_their_filter_out(ms):
+    R, V = 8, 6000
+    g = np.random.default_rng(12)
+    t = torch.from_numpy((2 * g.standard_normal((R, V))).astype(np.float32))
+    u = _uniform(g, R)
+    nan = np.float32(np.nan)
+    par = dict(temperature=np.array([nan, 1, 1, 1, nan, 0.5, 1, -np.inf], np.float32),
+               top_k=np.array([0, -5, -2 ** 31, 2 ** 31 - 1, 3, 40, V, 1], np.int32),
+               top_p=np.array([nan, nan, 0.5, np.inf, 0.5, nan, -np.inf, 0.5], np.float32),
+               min_p=np.array([nan, nan, -1, nan, 0.5, nan, 0, np.inf], np.float32))
+    for dtype in DTYPES:
+        z = t.to(DTYPES[dtype])
+        tok, probs = ms.sample(z.cuda(), dev(u), **_on(par), return_probs=True)
+        want, wp = sp.sample(z.float().numpy(), u, **par)
+        np.testing.assert_array_equal(host(tok), want)
+        _assert_probs(host(probs), wp)
+
+
 def test_random_numbers_outside_their_range_are_clamped(ms):
     z = torch.randn(4, 9000, device="cuda")
     top_k = torch.tensor([0, 50, 0, 50], dtype=torch.int32, device="cuda")
