@@ -288,7 +288,6 @@ struct SampleSmem {
     uint32_t wcnt[SP_WARPS];
     uint32_t sel_cnt;
     uint32_t nb0, nb1, nn;                    // the border's intervals and their tokens
-    uint32_t dropped;                         // ties behind the border
     uint32_t cut_idx;                         // broadcast: index of the last tied token kept
     int last;
     uint32_t keep;
@@ -301,9 +300,6 @@ struct SpChunk {
     TL* buf;
     int mis, n, nvec, begin;
     __device__ __forceinline__ int index(int vec, int e) const { return begin + vec * SpElem<TL>::VEC + e - mis; }
-    __device__ __forceinline__ void load(int vec, float (&v)[SpElem<TL>::VEC]) const {
-        SpElem<TL>::unpack(reinterpret_cast<const uint4*>(buf)[vec], v);
-    }
     // a vector, of -inf at and behind `end`
     __device__ __forceinline__ uint4 raw_to(int vec, int end) const {
         constexpr uint32_t kNone = sizeof(TL) == 2 ? 0xff80ff80u : 0xff800000u;
@@ -888,17 +884,15 @@ __device__ void pull_list(SampleSmem& sm, const uint32_t* ccnt, int n) {
 }
 
 // The border token of a list in index order: the k-th of the descending order
-// (k > 0), or the first at which A plus the running weight reaches the target
+// (k > 0), or the first at which the running weight reaches the target
 // (entries under `least` weigh nothing).  Returns its composite key, with a
-// zero index part where no tie of it stays behind; `dropped` counts the ties
-// that do.  srt is scratch for n keys.  All threads of the leader call it.
+// zero index part where no tie of it stays behind.  srt is scratch for n keys.
+// All threads of the leader call it.
 __device__ unsigned long long border_of(SampleSmem& sm, const unsigned long long* lst, unsigned long long* srt, int n,
-                                        int ksh, const SpScale& sc, unsigned long long least, uint32_t k, double A,
-                                        double target, uint32_t& dropped) {
+                                        int ksh, const SpScale& sc, unsigned long long least, uint32_t k, double want) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (n + SP_THREADS - 1) / SP_THREADS;
     const int nwarps = min(SP_WARPS, (n + 32 * per - 1) / (32 * per));
-    const double want = target - A;
     if (n > 128) {
         // few distinct logits (bf16): count each, and take the border's ties in index order
         uint32_t kmin = 0xffffffffu, kmax = 0;
@@ -941,7 +935,7 @@ __device__ unsigned long long border_of(SampleSmem& sm, const unsigned long long
                 own += m[j];
             }
             block_runs(sm, own, SP_WARPS, start, end, total);
-            const double goal = k > 0 ? static_cast<double>(min(k, static_cast<uint32_t>(n))) : want > 0.0 ? want : 0x1p-64;
+            const double goal = k > 0 ? static_cast<double>(min(k, static_cast<uint32_t>(n))) : want;
             if (start < goal && end >= goal) {
                 int at = -1;
                 double acc = start, before = start;
@@ -981,18 +975,14 @@ __device__ unsigned long long border_of(SampleSmem& sm, const unsigned long long
                 if (i < n && (static_cast<uint32_t>(lst[i] >> 32) >> ksh) == key && ++ex == keep) sm.sel_key = lst[i];
             }
             __syncthreads();
-            dropped = ties - keep;
             const unsigned long long cut = sm.sel_key;
             __syncthreads();
-            return dropped ? cut : cut & 0xffffffff00000000ull;
+            return keep < ties ? cut : cut & 0xffffffff00000000ull;
         }
     }
     __syncthreads();
     sort_list(sm, lst, srt, n);
-    if (tid == 0) {
-        sm.keep = k > 0 ? min(k, static_cast<uint32_t>(n)) : want > 0.0 ? n : 1;
-        sm.dropped = 0;
-    }
+    if (tid == 0) sm.keep = k > 0 ? min(k, static_cast<uint32_t>(n)) : n;
     if (k == 0) {
         double w[SP_PER], own = 0.0, start, end, total;
 #pragma unroll
@@ -1017,13 +1007,9 @@ __device__ unsigned long long border_of(SampleSmem& sm, const unsigned long long
     __syncthreads();
     const int at = max(0, static_cast<int>(sm.keep) - 1);
     const unsigned long long cut = srt[at];
-    uint32_t drop = 0;
-    for (int j = tid; j < n; j += SP_THREADS) drop += j > at && srt[j] >> 32 == cut >> 32 ? 1u : 0u;
-    if (drop) atomicAdd(&sm.dropped, drop);
-    __syncthreads();
-    dropped = sm.dropped;
-    __syncthreads();
-    return dropped ? cut : cut & 0xffffffff00000000ull;
+    bool behind = false;
+    for (int j = tid; j < n; j += SP_THREADS) behind |= j > at && srt[j] >> 32 == cut >> 32;
+    return __syncthreads_or(behind) ? cut : cut & 0xffffffff00000000ull;
 }
 
 struct SpRow {
@@ -1081,8 +1067,7 @@ __device__ void draw_from_list(SampleSmem& sm, int n, int ksh, float lcut, const
         }
         cut = max(least, srt[nk - 1]);
     } else if (r.by_k || r.by_p) {
-        uint32_t drop;
-        if (r.by_k) cut = max(least, border_of(sm, lst, srt, n, ksh, sc, least, static_cast<uint32_t>(r.k), 0.0, 0.0, drop));
+        if (r.by_k) cut = max(least, border_of(sm, lst, srt, n, ksh, sc, least, static_cast<uint32_t>(r.k), 0.0));
         if (r.by_p) {
             double S = S_all;
             if (r.by_k || S_all < 0.0) {
@@ -1094,7 +1079,7 @@ __device__ void draw_from_list(SampleSmem& sm, int n, int ksh, float lcut, const
                 block_runs(sm, own, nwarps, start, end, S);
             }
             // tokens that top-k left out come behind the border in the order
-            cut = max(cut, border_of(sm, lst, srt, n, ksh, sc, least, 0, 0.0, fmax(r.p * S, 1e-9), drop));
+            cut = max(cut, border_of(sm, lst, srt, n, ksh, sc, least, 0, fmax(r.p * S, 1e-9)));
         }
     }
     if (tid == 0) sm.wx = 0.0;
