@@ -32,7 +32,7 @@
 // element and fp64 pass, 11 of them fp64 at two issue cycles.  Memory is not the
 // bound: the row is read once.  Measured at V = 129,280 (replayed in a graph):
 //   1 bf16 row, all filters                       7.7 us
-//   32 fp32 rows, top-p (3 of them wide)           57 us
+//   32 fp32 rows, top-p (3 of them wide)           50 us
 //   64 bf16 rows, temperature, probs written       36 us  (1.4 TB/s)
 //   512 bf16 rows, filters of every kind          131 us  (1.0 TB/s)
 //   verification of 32 x 4 bf16 rows, top-p        91 us
@@ -283,6 +283,8 @@ struct SampleSmem {
     float cmax[SP_MAXC], cmin[SP_MAXC];       // every CTA's maximum, and the least of its threads' maxima
     uint32_t ccnt[4][SP_MAXC];                // every CTA's count, of each of up to four gathers
     uint32_t tie[SP_MAXC];
+    unsigned long long few[32];               // a window's last tokens, this CTA's
+    uint32_t nfew;
     float wmax[SP_WARPS], wmin[SP_WARPS];
     uint16_t order[SP_CAP];                   // leader: list entries by bucket
     uint32_t wcnt[SP_WARPS];
@@ -1540,16 +1542,82 @@ __device__ SpWindow make_window(SampleSmem& sm, uint32_t* ccnt, const SpChunk<TL
     return w;
 }
 
-// The border key of a window: with k > 0 the key at which the count A of the
-// tokens above the window plus the running count reaches k, else the one at
-// which the weight A above it plus the running weight reaches the target.
-// SP_BINS key ranges at a time: counts times the weights of a range's ends
-// bound its running sums, so that exact sums are needed of one range only; a
-// range of a single key is exact.  keep: how many of the `ties` tokens of that
-// key are on this side of the border.  All threads of the cluster call it.
+// A bit per element of vector i that equals tau.
 template <typename TL>
-__device__ uint32_t refine(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
-                           const SpWindow& w, bool by_count, double A, double target, uint32_t& keep, uint32_t& ties) {
+__device__ __forceinline__ uint32_t tie_mask(const SpChunk<TL>& ck, int i, float tau) {
+    constexpr int VEC = SpElem<TL>::VEC;
+    const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[i];
+    uint32_t mask = 0;
+    if (SpElem<TL>::any_eq(raw, tau)) {
+        float v[VEC];
+        SpElem<TL>::unpack(raw, v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) mask |= (v[e] == tau ? 1u : 0u) << e;
+    }
+    return mask;
+}
+
+// Index of the keep-th token with logit tau, in index order (two cluster
+// barriers).
+template <typename TL>
+__device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, const SpWindow& win, float tau,
+                         uint32_t keep) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int q0, q1;
+    warp_segment(ck.nvec, warp, q0, q1);
+    // this warp's ties, in index order along lanes and steps of 32 entries or vectors
+    const int first = win.listed ? static_cast<int>(win.start) : q0;
+    const int last = win.listed ? static_cast<int>(win.start + win.count) : q1;
+    auto ties_at = [&](int i) -> uint32_t {   // a bit per element of entry or vector i
+        if (i >= last) return 0;
+        if (win.listed) return composite_value(sm.loc[i]) == tau ? 1u : 0u;
+        return tie_mask<TL>(ck, i, tau);
+    };
+    uint32_t n = 0;
+    for (int i = first + lane; i < last; i += 32) n += __popc(ties_at(i));
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) sm.wcnt[warp] = n;
+    __syncthreads();
+    uint32_t tot = 0, before = 0;
+    for (int w = 0; w < SP_WARPS; ++w) {
+        if (w < warp) before += sm.wcnt[w];
+        tot += sm.wcnt[w];
+    }
+    if (tid < static_cast<int>(C)) st_cluster_s32(&sm.tie[rank], tid, static_cast<int>(tot));
+    cluster_sync_warp0();
+    for (uint32_t r = 0; r < rank; ++r) before += sm.tie[r];
+    if (keep > before && keep <= before + n) {
+        uint32_t left = keep - before;   // 1-based
+        for (int i0 = first; i0 < last; i0 += 32) {
+            uint32_t mask = ties_at(i0 + lane);
+            const uint32_t mine = __popc(mask);
+            uint32_t t;
+            const uint32_t ex = lanes_before(mine, lane, t);
+            if (ex + mine >= left && ex < left) {
+                uint32_t skip = left - ex - 1;
+                while (skip--) mask &= mask - 1;
+                const int idx = win.listed ? composite_index(sm.loc[i0 + lane]) : ck.index(i0 + lane, __ffs(mask) - 1);
+                for (uint32_t r = 0; r < C; ++r) st_cluster_s32(&sm.cut_idx, r, idx);
+            }
+            if (t >= left) break;
+            left -= t;
+        }
+    }
+    cluster_sync_all();
+    return static_cast<int>(sm.cut_idx);
+}
+
+// The border of a window, as border_of() returns one: with by_count the token
+// at which the count A of the tokens above the window plus the running count
+// reaches the target, else the one at which the weight A above it plus the
+// running weight does.  SP_BINS key ranges at a time: counts times the weights
+// of a range's ends bound its running sums, so that exact sums are needed of one
+// range only; a range of a single key is exact, and one of up to 32 tokens is
+// sorted (without that the 32 fp32 rows of top-p took 56 us instead of 50).
+// dropped: the ties behind the border.  All threads of the cluster call it.
+template <typename TL>
+__device__ unsigned long long refine(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale& sc, uint32_t rank, uint32_t C,
+                           const SpWindow& w, bool by_count, double A, double target, uint32_t& dropped) {
     constexpr int KSH = SpElem<TL>::KSH;
     const int tid = threadIdx.x, lane = tid & 31;
     uint32_t khi = order_key(w.top) >> KSH, klo = order_key(w.bot) >> KSH;
@@ -1619,10 +1687,12 @@ __device__ uint32_t refine(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale&
             }
             __syncthreads();
             if (sh == 0) {
-                ties = sm.sel_cnt;
+                const uint32_t ties = sm.sel_cnt;
                 const double need = ceil((target - sm.sel_before) / sm.sel_w);
-                keep = need < 1.0 ? 1u : need >= static_cast<double>(ties) ? ties : static_cast<uint32_t>(need);
-                return khi - b1;
+                const uint32_t keep = need < 1.0 ? 1u : need >= static_cast<double>(ties) ? ties : static_cast<uint32_t>(need);
+                const float tau = key_logit<TL>(khi - b1);
+                dropped = keep < ties ? ties - keep : 0u;
+                return composite(tau, dropped ? tie_index<TL>(sm, ck, rank, C, w, tau, keep) : -1);
             }
             A = sm.sel_before;
             khi -= b1 << sh;
@@ -1653,73 +1723,50 @@ __device__ uint32_t refine(SampleSmem& sm, const SpChunk<TL>& ck, const SpScale&
             khi = bot - 1;
             klo = end - klo > span ? end - span : klo;
         }
-        // (every CTA has read the counts before share_two()'s barrier, and reads the tables before the next counts')
-    }
-}
-
-// A bit per element of vector i that equals tau.
-template <typename TL>
-__device__ __forceinline__ uint32_t tie_mask(const SpChunk<TL>& ck, int i, float tau) {
-    constexpr int VEC = SpElem<TL>::VEC;
-    const uint4 raw = reinterpret_cast<const uint4*>(ck.buf)[i];
-    uint32_t mask = 0;
-    if (SpElem<TL>::any_eq(raw, tau)) {
-        float v[VEC];
-        SpElem<TL>::unpack(raw, v);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) mask |= (v[e] == tau ? 1u : 0u) << e;
-    }
-    return mask;
-}
-
-// Index of the keep-th token with logit tau, in index order (two cluster
-// barriers).
-template <typename TL>
-__device__ int tie_index(SampleSmem& sm, const SpChunk<TL>& ck, uint32_t rank, uint32_t C, const SpWindow& win, float tau,
-                         uint32_t keep) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int q0, q1;
-    warp_segment(ck.nvec, warp, q0, q1);
-    // this warp's ties, in index order along lanes and steps of 32 entries or vectors
-    const int first = win.listed ? static_cast<int>(win.start) : q0;
-    const int last = win.listed ? static_cast<int>(win.start + win.count) : q1;
-    auto ties_at = [&](int i) -> uint32_t {   // a bit per element of entry or vector i
-        if (i >= last) return 0;
-        if (win.listed) return composite_value(sm.loc[i]) == tau ? 1u : 0u;
-        return tie_mask<TL>(ck, i, tau);
-    };
-    uint32_t n = 0;
-    for (int i = first + lane; i < last; i += 32) n += __popc(ties_at(i));
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) sm.wcnt[warp] = n;
-    __syncthreads();
-    uint32_t tot = 0, before = 0;
-    for (int w = 0; w < SP_WARPS; ++w) {
-        if (w < warp) before += sm.wcnt[w];
-        tot += sm.wcnt[w];
-    }
-    if (tid < static_cast<int>(C)) st_cluster_s32(&sm.tie[rank], tid, static_cast<int>(tot));
-    cluster_sync_warp0();
-    for (uint32_t r = 0; r < rank; ++r) before += sm.tie[r];
-    if (keep > before && keep <= before + n) {
-        uint32_t left = keep - before;   // 1-based
-        for (int i0 = first; i0 < last; i0 += 32) {
-            uint32_t mask = ties_at(i0 + lane);
-            const uint32_t mine = __popc(mask);
-            uint32_t t;
-            const uint32_t ex = lanes_before(mine, lane, t);
-            if (ex + mine >= left && ex < left) {
-                uint32_t skip = left - ex - 1;
-                while (skip--) mask &= mask - 1;
-                const int idx = win.listed ? composite_index(sm.loc[i0 + lane]) : ck.index(i0 + lane, __ffs(mask) - 1);
-                for (uint32_t r = 0; r < C; ++r) st_cluster_s32(&sm.cut_idx, r, idx);
+        // (every CTA has read the counts before share_two()'s barrier, and reads the tables before the next one)
+        if constexpr (KSH == 0) {   // (a bf16 window has few values)
+            if (!w.listed) continue;
+            if (tid == 0) sm.nfew = 0;
+            __syncthreads();
+            for (uint32_t i = tid; i < w.mine; i += SP_THREADS) {
+                const unsigned long long k = sm.loc[i];
+                const uint32_t key = static_cast<uint32_t>(k >> 32) >> KSH;
+                if (key < klo || key > khi) continue;
+                const uint32_t at = atomicAdd(&sm.nfew, 1u);
+                if (at < 32) sm.few[at] = k;
             }
-            if (t >= left) break;
-            left -= t;
+            cluster_sync_warp0();
+            uint32_t all = 0, cta = 0, slot = 0;   // where this lane's token is
+            for (uint32_t c = 0; c < C; ++c) {
+                uint32_t x;
+                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(sp_mapa(&sm.nfew, c)) : "memory");
+                if (static_cast<uint32_t>(lane) >= all) {
+                    cta = c;
+                    slot = lane - all;
+                }
+                all += x;
+            }
+            if (all == 0 || all > 32) continue;
+            // the few in order (all different), their running weight on top of A
+            const bool has = static_cast<uint32_t>(lane) < all;
+            if (tid < 32) {
+                unsigned long long k = 0;
+                if (has) asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(sp_mapa(&sm.few[slot], cta)) : "memory");
+                uint32_t before = 0;
+    #pragma unroll
+                for (int i = 0; i < 32; ++i) before += __shfl_sync(0xffffffffu, k, i) > k ? 1u : 0u;
+                if (has) sm.lst[before] = k;
+            }
+            __syncthreads();
+            const unsigned long long k = has ? sm.lst[lane] : 0ull;
+            const double run = A + warp_scan(has ? sc.weight(composite_value(k)) : 0.0, lane);
+            const unsigned reach = __ballot_sync(0xffffffffu, has && run >= target);
+            const int end = reach ? __ffs(reach) - 1 : static_cast<int>(all) - 1;
+            const unsigned long long cut = __shfl_sync(0xffffffffu, k, end);
+            dropped = __popc(__ballot_sync(0xffffffffu, has && lane > end && k >> 32 == cut >> 32));
+            return dropped ? cut : cut & 0xffffffff00000000ull;
         }
     }
-    cluster_sync_all();
-    return static_cast<int>(sm.cut_idx);
 }
 
 // Index of the keep-th of this CTA's elements equal to tau.
@@ -2094,11 +2141,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
                 const SpWindow win = make_window<TL>(sm, sm.ccnt[2], ck, rank, C, lcut, bins, kt.b, kt.b);
                 cut = composite(lcut, -1);   // (fewer than k)
                 if (win.all) {
-                    uint32_t keep, ties;
-                    const float v = key_logit<TL>(
-                        refine<TL>(sm, ck, sc, rank, C, win, true, static_cast<double>(kt.above), static_cast<double>(r.k), keep, ties));
-                    dropped = ties - keep;
-                    cut = composite(v, dropped ? tie_index<TL>(sm, ck, rank, C, win, v, keep) : -1);
+                    cut = refine<TL>(sm, ck, sc, rank, C, win, true, static_cast<double>(kt.above), static_cast<double>(r.k), dropped);
                 }
             }
             if (r.by_p) {
@@ -2115,9 +2158,8 @@ __global__ void __launch_bounds__(SP_THREADS, 1024 / SP_THREADS) sample_kernel(c
                 share_sums(sm.rsum, mine_above, rank, C);
                 const double A = table_sum(sm.rsum, C, lane);
                 const SpWindow win = make_window<TL>(sm, sm.ccnt[3], ck, rank, C, kth, bins, nu.b0, nu.b1);
-                uint32_t keep, ties;
-                const float v = key_logit<TL>(refine<TL>(sm, ck, sc, rank, C, win, false, A, target, keep, ties));
-                cut = max(cut, composite(v, keep < ties ? tie_index<TL>(sm, ck, rank, C, win, v, keep) : -1));
+                uint32_t behind;
+                cut = max(cut, refine<TL>(sm, ck, sc, rank, C, win, false, A, target, behind));
                 tau = composite_value(cut);
                 const double mine_border = border_part<TL>(sm, ck, win, cut, sc);
                 share_sums(sm.wsum, mine_above + mine_border, rank, C);
