@@ -581,7 +581,10 @@ __device__ SpKth kth_interval(SampleSmem& sm, const SpChunk<TL>& ck, const SpSca
         if (w < warp) ex += sm.wcnt[w];
         tot += sm.wcnt[w];
     }
-    if (tot < k) return SpKth{SP_BINS - 1, tot};
+    if (tot < k) {
+        __syncthreads();   // wcnt has been read: the caller's gather() writes it
+        return SpKth{SP_BINS - 1, tot};
+    }
 #pragma unroll
     for (int j = 0; j < SP_BPT; ++j) {
         if (ex < k && ex + n[j] >= k) {

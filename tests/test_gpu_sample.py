@@ -301,6 +301,25 @@ def test_borders_among_small_values(ms, par, dtype):
         np.testing.assert_array_equal(host(n), wn)
 
 
+@pytest.mark.parametrize("temperature,k", [(0.05, 2500), (0.3, 20000), (0.3, 49999)], ids=["fewer", "last", "all"])
+@pytest.mark.parametrize("R", [5, 48])
+def test_wide_top_k_whose_kth_token_is_not_counted(ms, R, temperature, k):
+    """fp32 rows whose k-th token lies in the uncounted last interval, or that hold fewer than k tokens above the cut;
+    50,000 fp32 are 3,126 vectors a CTA of 4 in warp segments of 224, so that the last two warps have none."""
+    V = 50000
+    g = np.random.default_rng(k)
+    z = (g.standard_normal((R, V)) * (1.0 if k == 2500 else 3.0)).astype(np.float32)
+    u = _uniform(g, R)
+    for top_p in (None, 0.95):
+        par = dict(temperature=np.full(R, temperature, np.float32), top_k=np.full(R, k, np.int32))
+        if top_p:
+            par["top_p"] = np.full(R, top_p, np.float32)
+        tok, probs = ms.sample(dev(z), dev(u), **_on(par), return_probs=True)
+        want, wp = sp.sample(z, u, **par)
+        np.testing.assert_array_equal(host(tok), want)
+        _assert_probs(host(probs), wp)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_sample_from_any_element_offset(ms, dtype):
     """Rows and outputs that start at any element, filters that take every path."""
