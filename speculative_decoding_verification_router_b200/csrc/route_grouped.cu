@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
                 c1 += __ldg(a.bias + e1);
                 c2 += __ldg(a.bias + e2);
                 err += 3e-7f * (fabsf(c1) + fabsf(c2));
+                odd |= !(c1 == c1);   // a NaN bias: the lane's first key, and comparisons with it would lose its group
             }
             if (P > 2 && rg_value(best[1] & ~255) - rg_value(best[2] & ~255) <= fabsf(rg_value(best[1] & ~255)) * 4e-5f + 8e-6f)
                 err += a.bias ? fabsf(c2) * 4e-5f + 8e-6f : 1e-5f * fabsf(z2) * (a.sigmoid ? 1.f : 4.f * c2);

@@ -159,6 +159,21 @@ def test_many_tokens_with_close_scores(ms, E, groups, score, dtype):
             assert bool(((w.double() - rw).abs() <= REL * rw + 1e-37)[sure].all())
 
 
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(8, 2), (8, 4), (40, 2), (64, 2), (64, 4), (120, 4), (256, 2), (256, 4)])
+def test_nan_bias_in_groups_of_several_lanes(ms, E, groups, score, group_top):
+    g = np.random.default_rng(E + groups)
+    z = 2 * g.standard_normal((65, E)).astype(np.float32)
+    for n in (1, 2, E // 4):
+        for values in ([np.nan], [-np.nan], [np.nan, np.inf, -np.inf]):
+            bias = (0.1 * g.standard_normal(E)).astype(np.float32)
+            bias[g.choice(E, n, replace=False)] = g.choice(np.array(values, np.float32), n)
+            for tg in {1, groups // 2, groups - 1}:
+                _check(ms, z, min(6, tg * (E // groups)), "f32", bias=bias, score=score, n_groups=groups, topk_groups=tg,
+                       group_top=group_top, renormalize=True)
+
+
 def test_softmax_without_groups_is_route_topk(ms):
     g = np.random.default_rng(1)
     H, E, T = 256, 64, 50
