@@ -427,6 +427,10 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
             if (P > 2 && rg_value(best[1] & ~255) - rg_value(best[2] & ~255) <= fabsf(rg_value(best[1] & ~255)) * 4e-5f + 8e-6f)
                 err += a.bias ? fabsf(c2) * 4e-5f + 8e-6f : 1e-5f * fabsf(z2) * (a.sigmoid ? 1.f : 4.f * c2);
             if (P == 1) c2 = -INFINITY;
+            // equal keys come to the lower expert first, which may have the smaller score
+            const float larger = fmaxf(c1, c2);
+            c2 = fminf(c1, c2);
+            c1 = larger;
             for (int o = 1; o < L; o <<= 1) {
                 const float o1 = __shfl_xor_sync(0xffffffffu, c1, o), o2 = __shfl_xor_sync(0xffffffffu, c2, o);
                 merge_two(c1, c2, o1, o2);

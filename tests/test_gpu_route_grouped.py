@@ -174,6 +174,29 @@ def test_nan_bias_in_groups_of_several_lanes(ms, E, groups, score, group_top):
                        group_top=group_top, renormalize=True)
 
 
+def _logit(s):
+    return np.log(s / (1 - s)).astype(np.float32)
+
+
+@pytest.mark.parametrize("bias", [0.0, 2.0 ** -30, None])
+def test_a_groups_best_behind_a_lower_expert_of_the_same_coarse_score(ms, bias):
+    """Scores of one step of 16 bits come to the lower expert first, the smaller one here."""
+    E, step = 64, 2.0 ** -16                 # of scores in [1/2, 1)
+    base = np.floor(0.6 / step) * step
+    b = None if bias is None else np.full(E, bias, np.float32)
+    kw = dict(bias=b, score="sigmoid")
+    z = np.tile(-1 - 0.01 * np.arange(E, dtype=np.float32), (1, 1))
+    z[0, [0, 1, 8]] = _logit(base + step * np.array([0.1, 0.9, 0.5]))
+    _check(ms, z, 3, "f32", n_groups=8, topk_groups=1, group_top=1, **kw)
+    z[0, [1, 6, 2, 9]] = [-1, *_logit(base + step * np.array([0.9, 0.1, 0.5]))]   # in another lane's group
+    _check(ms, z, 3, "f32", n_groups=8, topk_groups=1, group_top=1, **kw)
+    # groups of two lanes, each of which has its two best the wrong way round
+    z = np.tile(-1 - 0.01 * np.arange(E, dtype=np.float32), (1, 1))
+    z[0, [0, 1, 8, 9, 16, 17]] = _logit(base + step * np.array([0.46, 0.69, 0.23, 0.92, 0.76, 0.76]))
+    _check(ms, z, 4, "f32", n_groups=4, topk_groups=1, group_top=2, **kw)
+    _check(ms, z, 4, "f32", n_groups=2, topk_groups=1, group_top=2, **kw)
+
+
 def test_softmax_without_groups_is_route_topk(ms):
     g = np.random.default_rng(1)
     H, E, T = 256, 64, 50
