@@ -409,23 +409,30 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
             odd |= sizeof(TL) == 4 && ((low ^ high) & ~255) == 0;
             odd |= a.sigmoid ? fabsf(rg_value(low & ~255)) > 30.f : rg_value(low & ~255) - m < -80.f;
         } else {
-            // the scores of the lane's two best, in fp32 from their logits; where the second and third are not told
-            // apart, the second may be up to their coarse error larger
+            // The scores of the lane's two best, in fp32 from their logits.  One is off by at most ev: by sigmoid
+            // 2.6e-7, by softmax 3.7e-6 of itself (most of it the sum's) and 5e-8 of the largest, with a bias two
+            // roundings more.  Where the second and third keys are not told apart, the third and fourth may be the
+            // larger ones, each by at most disp, a step of the keys (2^-15 relative).  A group's sum has two scores of
+            // any of its lanes, and a comparison two groups, of which the one left out may lack two displaced ones:
+            // 4 ev + 2 disp, and twice that, as the lane with the largest ev need not be the one with the largest disp.
             const TL* row = static_cast<const TL*>(a.logits) + static_cast<size_t>(t) * a.E;
             const int e1 = 255 - (best[0] & 255), e2 = P > 1 ? 255 - (best[1] & 255) : e1;
             const float z1 = rg_load(row + e1), z2 = rg_load(row + e2);
             odd |= a.sigmoid ? fabsf(z1) > 30.f : z1 - m < -80.f;
             float c1 = a.sigmoid ? rg_rcp(1.f + rg_ex2(z1 * -kLog2e)) : rg_ex2((z1 - m) * kLog2e) * norm;
             float c2 = a.sigmoid ? rg_rcp(1.f + rg_ex2(z2 * -kLog2e)) : rg_ex2((z2 - m) * kLog2e) * norm;
-            float err = a.sigmoid ? 1.6e-6f : 8e-6f * (c1 + c2);
+            float ev = a.sigmoid ? 2.6e-7f : fmaf(fmaxf(c1, c2), 3.7e-6f, 5e-8f * norm), disp = 0.f;
             if (a.bias) {
                 c1 += __ldg(a.bias + e1);
                 c2 += __ldg(a.bias + e2);
-                err += 3e-7f * (fabsf(c1) + fabsf(c2));
+                ev += 1.2e-7f * fmaxf(fabsf(c1), fabsf(c2));
                 odd |= !(c1 == c1);   // a NaN bias: the lane's first key, and comparisons with it would lose its group
             }
-            if (P > 2 && rg_value(best[1] & ~255) - rg_value(best[2] & ~255) <= fabsf(rg_value(best[1] & ~255)) * 4e-5f + 8e-6f)
-                err += a.bias ? fabsf(c2) * 4e-5f + 8e-6f : 1e-5f * fabsf(z2) * (a.sigmoid ? 1.f : 4.f * c2);
+            if (P > 2 && rg_value(best[1] & ~255) - rg_value(best[2] & ~255) <= fabsf(rg_value(best[1] & ~255)) * 4e-5f + 8e-6f) {
+                disp = a.bias ? fabsf(c2) * 3.2e-5f : fabsf(z2) * (a.sigmoid ? 1e-5f : 4e-5f * c2);
+                odd |= !(fabsf(z2) < 1e4f);   // a step of the logit is more than a small part of its weight
+            }
+            float err = 8.f * ev + 4.f * disp;
             if (P == 1) c2 = -INFINITY;
             // equal keys come to the lower expert first, which may have the smaller score
             const float larger = fmaxf(c1, c2);

@@ -197,6 +197,32 @@ def test_a_groups_best_behind_a_lower_expert_of_the_same_coarse_score(ms, bias):
     _check(ms, z, 4, "f32", n_groups=2, topk_groups=1, group_top=2, **kw)
 
 
+def _close_fours(E, base, low, high, between, rest):
+    """Two experts at base + low, two behind them at base + high, and two of the second group in between."""
+    v = np.full((1, E), rest, np.float32)
+    v[0, [0, 1]], v[0, [2, 3]], v[0, [E // 8, E // 8 + 1]] = np.float32(base + low), np.float32(base + high), np.float32(base + between)
+    return v
+
+
+def test_four_close_scores_in_one_lane(ms):
+    """Four experts of one group within one step of the coarse scores, the two larger behind: both of the group's best
+    are short by up to a step, and the second group lies between."""
+    E = 256
+    kw = dict(n_groups=8, topk_groups=1, group_top=2)
+    # by the bias alone (scores 1/2)
+    bias = _close_fours(E, 0.0, 0.5, 0.50003, 0.500028, -0.4)[0]
+    _check(ms, np.zeros((1, E), np.float32), 2, "f32", bias=bias, score="sigmoid", **kw)
+    # by the logits: steps of 2^-15 relative
+    for d in (245, 249, 251, 253):
+        z = _close_fours(E, 1.0, 0.0, 255 * 2.0 ** -23, d * 2.0 ** -23, -2.0)
+        _check(ms, z, 2, "f32", bias=None, score="sigmoid", **kw)
+    for b in (4.0, 8.0, 64.0, 16384.0):
+        z = _close_fours(E, b, 0.0, b * 255 * 2.0 ** -23, b * 230 * 2.0 ** -23, b - 8)
+        _check(ms, z, 2, "f32", bias=None, score="softmax", **kw)
+        bias = np.zeros(E, np.float32)
+        _check(ms, z, 2, "f32", bias=bias, score="softmax", **kw)
+
+
 def test_softmax_without_groups_is_route_topk(ms):
     g = np.random.default_rng(1)
     H, E, T = 256, 64, 50
