@@ -123,6 +123,8 @@ MS_API ms_status moe_route_topk_tensor(const void* xhat, const float* w_router, 
  *   lower expert;  topk_w: s of the chosen experts (the bias only selects),
  *   divided by their sum when renormalize != 0, times scale.
  * The choice is that of scores in fp64: it does not depend on fp32 rounding.
+ * Different logits whose fp64 scores are equal (sigmoid of large ones, logits
+ * around zero that differ by less than 1e-16) are equal values.
  * topk_w is evaluated in fp32 (about 1e-6 relative).  A logit of -inf or NaN
  * masks its expert: s = 0, ranked behind every other expert of the chosen
  * groups (a masked expert counts 0 in its group's score, a group without any

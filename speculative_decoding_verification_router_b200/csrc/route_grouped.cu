@@ -252,6 +252,14 @@ __device__ __forceinline__ float rg_exp_diff(float a, float b) {
 }
 constexpr int kNoKey = static_cast<int>(0x80000000u);
 
+// Without a bias the logits order the scores, as long as different logits have
+// different fp64 scores.  They may not among logits under kTiny (above it fp32
+// neighbours are 2^-44 apart, 2^-46 in their scores) and, by sigmoid, where
+// 1 - s is small: at 20 neighbours of fp32 are 3.9e-15 apart, 35 steps of fp64,
+// at 24 often none; at 30 neighbours of bf16 are 1e-14 apart.  Ties of scores go
+// to the lower expert, which the exact form sees to.
+constexpr float kTiny = 0x1p-20f;
+
 __device__ __forceinline__ void rg_swap(int& a, int& b) {   // larger first
     const int hi = max(a, b), lo = min(a, b);
     a = hi;
@@ -389,7 +397,8 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
     }
 
     // groups: the two best of each, their rank among the groups
-    bool inside = true;
+    bool inside = true, ties = false;   // ties: equal fp64 scores of different logits may matter
+    constexpr float kFar = sizeof(TL) == 4 ? 20.f : 30.f;
     if (a.topk_groups < a.groups) {
         const int L = 8 / a.groups, mine = sub / L;
         bool& in = inside;
@@ -407,7 +416,9 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
                 high = max(high, __shfl_xor_sync(0xffffffffu, high, o));
             }
             odd |= sizeof(TL) == 4 && ((low ^ high) & ~255) == 0;
-            odd |= a.sigmoid ? fabsf(rg_value(low & ~255)) > 30.f : rg_value(low & ~255) - m < -80.f;
+            const float lowest = rg_value(low & ~255);
+            odd |= a.sigmoid ? lowest > kFar || lowest < -30.f : lowest - m < -80.f;
+            ties = fabsf(lowest) < kTiny;
         } else {
             // The scores of the lane's two best, in fp32 from their logits.  One is off by at most ev: by sigmoid
             // 2.6e-7, by softmax 3.7e-6 of itself (most of it the sum's) and 5e-8 of the largest, with a bias two
@@ -484,19 +495,27 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
     }
     if (!a.bias) {
         close |= sizeof(TL) == 4 && next != kNoKey && ((kth ^ next) & ~255) == 0;
+        ties |= fabsf(rg_value(kth & ~255)) < kTiny;
+        if (ties) {
+#pragma unroll
+            for (int i = 0; i < NL * 8; ++i)
+                if (FULL || i < P) odd |= fabsf(zval(i)) < kTiny && zval(i) != 0.f;
+        }
     } else if (next != kNoKey) {
         const float vk = rg_value(kth & ~255), vn = rg_value(next & ~255);
         close |= !(vk - vn > fmaxf(fabsf(vk), fabsf(vn)) * 4e-5f + 8e-6f);
     }
     // the k, their order and weights: lane j of the token has candidate j.  Without a bias the logits order the
-    // scores, as long as those differ in fp64; with one, scores closer than their error go to the exact form.
+    // scores (but for tiny and far ones), with one, scores closer than their error are settled below.
     const bool has = sub < a.k && own != kNoKey;
     const int e = has ? 255 - (own & 255) : 0;
     const float ze = rg_load(static_cast<const TL*>(a.logits) + static_cast<size_t>(t) * a.E + e);
     const float x = a.sigmoid ? rg_exp_diff(0.f, ze) : rg_exp_diff(ze, m);
     float w = a.sigmoid ? 1.f / (1.f + x) : x / sum;
     const float c = a.bias ? w + __ldg(a.bias + e) : ze;
-    odd |= has && (a.sigmoid ? fabsf(ze) > 30.f : ze - m < -80.f);   // far scores: fp64's range is needed
+    // far scores need fp64's range
+    odd |= has && (a.sigmoid ? ze > (a.bias ? 30.f : kFar) || ze < -30.f : ze - m < -80.f);
+    odd |= has && !a.bias && fabsf(ze) < kTiny && ze != 0.f;
     int rank = 0;
     float wsum = 0.f;
 #pragma unroll

@@ -223,6 +223,46 @@ def test_four_close_scores_in_one_lane(ms):
         _check(ms, z, 2, "f32", bias=bias, score="softmax", **kw)
 
 
+@pytest.mark.parametrize("E", [60, 64, 256])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (4, 1), (4, 2)])
+def test_large_logits_whose_scores_are_equal(ms, E, groups, group_top):
+    """Neighbouring fp32 logits from about 24 up have equal sigmoid scores in 64 bits: the lower expert comes first."""
+    T = 400
+    g = np.random.default_rng(E)
+    z = (g.standard_normal((T, E)) - 3).astype(np.float32)
+    x = np.linspace(18, 30, T).astype(np.float32)
+    at = np.stack([g.choice(E, 4, replace=False) for _ in range(T)])
+    r = np.arange(T)
+    z[r, at[:, 0]] = x
+    z[r, at[:, 1]] = np.nextafter(x, np.float32(100))
+    z[r, at[:, 2]] = np.nextafter(x, np.float32(0))
+    z[::2][r[: T // 2], at[::2, 3]] = x[::2]
+    for k in (1, 2, 6):
+        for tg in {1, (groups + 1) // 2}:
+            _check(ms, z, k, "f32", bias=None, score="sigmoid", n_groups=groups, topk_groups=tg, group_top=group_top,
+                   renormalize=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [60, 64, 256])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (4, 1), (4, 2)])
+def test_tiny_logits_whose_scores_are_equal(ms, groups, group_top, E, score, dtype):
+    """Logits around zero that differ by less than 64-bit scores do: the lower expert comes first."""
+    T = 200
+    g = np.random.default_rng(E + groups)
+    kinds = np.array([0.0, -0.0, 1e-20, -1e-20, 1e-30, -1e-30, 1e-44, 3e-18, -2e-18])
+    z = kinds[g.integers(0, len(kinds), (T, E))]
+    z[:50, ::5] = g.standard_normal((50, len(range(0, E, 5))))          # some far from zero
+    z[50:100][g.random((50, E)) < 0.95] = -1.0                            # a few tiny ones among the best
+    z[100:150] = np.where(g.random((50, E)) < 0.7, 0.0, -1e-30)           # the border among zeros
+    z = z.astype(np.float32)
+    for k in (1, 2, 6):
+        for tg in {1, (groups + 1) // 2}:
+            _check(ms, z, k, dtype, bias=None, score=score, n_groups=groups, topk_groups=tg, group_top=group_top,
+                   renormalize=True)
+
+
 def test_softmax_without_groups_is_route_topk(ms):
     g = np.random.default_rng(1)
     H, E, T = 256, 64, 50
