@@ -516,6 +516,9 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
     // far scores need fp64's range
     odd |= has && (a.sigmoid ? ze > (a.bias ? 30.f : kFar) || ze < -30.f : ze - m < -80.f);
     odd |= has && !a.bias && fabsf(ze) < kTiny && ze != 0.f;
+    // two scores' errors: 1.9e-7 each by sigmoid; by softmax the fp32 sum's comes on top, at most 3.4e-6 of the two
+    // scores' difference (32 terms in sequence and three levels of lanes, 2.1e-6; the terms' own, 1.3e-6)
+    const float apart = a.sigmoid ? 1.2e-6f : 4.6e-6f;
     int rank = 0;
     float wsum = 0.f;
 #pragma unroll
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
         if (o < a.k) {
             rank += co > c || (co == c && eo < e) ? 1 : 0;
             wsum += wo;
-            if (a.bias) close |= has && eo != e && fabsf(co - c) < 1.2e-6f + fabsf(c) * 3e-7f;
+            if (a.bias) close |= has && eo != e && fabsf(co - c) < apart + fabsf(c) * 3e-7f;
         }
     }
     odd |= (sub < a.k && !has) || !(c == c);

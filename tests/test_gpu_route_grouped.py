@@ -263,6 +263,19 @@ def test_tiny_logits_whose_scores_are_equal(ms, groups, group_top, E, score, dty
                    renormalize=True)
 
 
+def test_softmax_sum_that_rounds_one_way(ms):
+    """31 weights of a little over half a step each are rounded up one by one in the fp32 sum, 1.8e-6 in all: a
+    neighbour whose score is its bias must not pass the largest by that."""
+    E = 256
+    z = np.full((1, E), -40.0, np.float32)
+    z[0, :32] = np.float32(np.log(6.05e-8))
+    z[0, 0] = 0.0
+    for n in (32, 33, 34, 35, 36):
+        bias = np.zeros(E, np.float32)
+        bias[100] = np.float32(1 - n * 2.0 ** -24)
+        _check(ms, z, 2, "f32", bias=bias, score="softmax")
+
+
 def test_softmax_without_groups_is_route_topk(ms):
     g = np.random.default_rng(1)
     H, E, T = 256, 64, 50
