@@ -283,7 +283,8 @@ MS_API ms_status spec_sample(const void* logits, ms_dtype logits_dtype, int T, i
  * committed[b,:] = the accepted drafts, the drawn token, then -1 padding;
  * n_committed[b] = how many of them are tokens: 1..K+1 (one less where the
  * drawn row has no logit above -inf: its token is -1).  A draft outside [0, V)
- * is rejected.
+ * is rejected.  draft_probs are 0 or more; an infinite or NaN one rejects its
+ * draft and leaves nothing of its token in max(p_j - q_j, 0).
  * logits: [B,K+1,V] fp32 or bf16 (any element alignment).  draft: [B,K]
  * int32.  draft_probs: [B,K,V] fp32 or NULL.  temperature, top_p, min_p: [B]
  * fp32, top_k: [B] int32, each NULL or as in spec_sample.  u: [B,K+1] fp32 in [0, 1), independent.

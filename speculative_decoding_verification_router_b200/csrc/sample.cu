@@ -1118,8 +1118,10 @@ __device__ void draw_from_list(SampleSmem& sm, int n, int ksh, float lcut, const
 #pragma unroll
             for (int e = 0; e < SP_PER; ++e) {
                 rw[e] = 0.0;
-                if (w[e] > 0.0)
-                    rw[e] = fmax(0.0, w[e] - static_cast<double>(__ldg(r.q + composite_index(lst[tid * per + e]))) * S);
+                if (w[e] > 0.0) {
+                    const double q = fabs(static_cast<double>(__ldg(r.q + composite_index(lst[tid * per + e]))));
+                    rw[e] = fmax(0.0, w[e] - q * S);   // (NaN: 0)
+                }
                 rown += rw[e];
             }
             block_runs(sm, rown, nwarps, rs, re, rt);
@@ -1373,8 +1375,12 @@ __device__ double segment_part(const SpChunk<TL>& ck, float tau, const SpScale& 
     return s0 + s1;
 }
 
-// w - q S, S as S 2^896 (q is 0 or more; an infinite or NaN one leaves nothing).
-__device__ __forceinline__ double residual(double w, float q, double S896) { return fma(-scaled_f64(q), S896, w); }
+// w - |q| S, S as S 2^896.  An infinite or NaN q becomes 2^128 or more and leaves nothing; without its sign, which a
+// NaN may have (0/0 on the host) and which would leave all of the row's weight to its token.
+__device__ __forceinline__ double residual(double w, float q, double S896) {
+    const int u = __float_as_int(q);
+    return fma(-__hiloint2double((u >> 3) & 0x0fffffff, u << 29), S896, w);
+}
 
 // One element of the residual max(w - q S, 0) of the weights at or above tau
 // (q NULL: of the weights).

@@ -420,6 +420,36 @@ def test_verify_sample_full_vocabulary(ms, par, with_q):
     np.testing.assert_array_equal(host(n), wn)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("par", [dict(temperature=1.5), dict(top_k=50), dict(temperature=1.5, top_p=0.97), dict(top_k=4000)],
+                         ids=["row", "list", "p", "k"])
+def test_draft_probs_that_are_infinite_or_nan(ms, par, dtype):
+    """They reject their draft and leave nothing of their tokens, whatever the sign of a NaN and the way of the row."""
+    B, K, V = 24, 2, 20011
+    g = np.random.default_rng(13)
+    z = torch.from_numpy((2 * g.standard_normal((B, K + 1, V))).astype(np.float32)).to(DTYPES[dtype])
+    zh = z.float().numpy()
+    q = np.exp(zh[:, :K] + g.standard_normal((B, K, V)))
+    q = (q / q.sum(-1, keepdims=True)).astype(np.float32)
+    d = zh[:, :K].argmax(-1).astype(np.int32)
+    bad = np.array([0x7fc00000, 0xffc00000, 0xffffffff, 0x7f800001, 0xff800001, 0x7f800000], np.uint32).view(np.float32)
+    best = np.argsort(-zh[:, :K], axis=-1)[..., :12]
+    for r in range(0, B, 2):
+        for j in range(K):
+            for i in range(1 if r % 4 else 0, 12):   # every other time the draft's own among them
+                q[r, j, best[r, j, i]] = bad[(r + i) % len(bad)]
+    q[1::2, :, ::97] = bad[g.integers(0, len(bad), q[1::2, :, ::97].shape)]
+    par = {n: np.full(B, v, np.int32 if n == "top_k" else np.float32) for n, v in par.items()}
+    u = _uniform(g, (B, K + 1))
+    cm, n = ms.verify_sample(z.cuda(), dev(d), dev(u), draft_probs=dev(q), **_on(par))
+    torch.cuda.synchronize()
+    # a u of 0 times an infinite probability is NaN: no acceptance either
+    with np.errstate(invalid="ignore"):
+        wcm, wn = sp.verify(zh, d, u, np.where(np.isfinite(q), q, np.inf).astype(np.float32), **par)
+    np.testing.assert_array_equal(host(cm), wcm)
+    np.testing.assert_array_equal(host(n), wn)
+
+
 def test_greedy_rows_verify_as_spec_verify_greedy(ms):
     B, K, V = 16, 3, 4096
     z = torch.randn(B, K + 1, V, device="cuda").bfloat16()
