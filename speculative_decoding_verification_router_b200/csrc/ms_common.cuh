@@ -168,6 +168,11 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool element_aligned(const void* p, ms_dtype dt) {
     return (reinterpret_cast<uintptr_t>(p) & (dt == MS_BF16 ? 1u : 3u)) == 0;
 }
+// Pointers to 4-byte elements (NULL is aligned).
+template <typename... P>
+inline bool words_aligned(const P*... p) {
+    return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
+}
 
 // ------------------------------------------------------------ device side
 // Wait for the kernel this one depends on (no-op when launched without PDL).

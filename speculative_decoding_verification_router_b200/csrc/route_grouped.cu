@@ -650,7 +650,7 @@ extern "C" ms_status moe_route_grouped(const void* logits, ms_dtype logits_dtype
     if (T <= 0 || E <= 0 || n_groups <= 0 || E % n_groups != 0) return MS_ERR_INVALID_ARG;
     if (topk_groups <= 0 || topk_groups > n_groups || group_top < 1 || group_top > 2) return MS_ERR_INVALID_ARG;
     if (k <= 0 || k > topk_groups * (E / n_groups)) return MS_ERR_INVALID_ARG;
-    if (!ms::element_aligned(logits, logits_dtype)) return MS_ERR_INVALID_ARG;
+    if (!ms::element_aligned(logits, logits_dtype) || !ms::words_aligned(select_bias, topk_idx, topk_w)) return MS_ERR_INVALID_ARG;
     if (E > ms::RG_MAXE || n_groups > 32 || k > 32) return MS_ERR_UNSUPPORTED;
     ms::RouteGroupedArgs a{logits,       select_bias,  T,     E,        n_groups, topk_groups, group_top, k,
                            score == MS_SIGMOID, renormalize != 0, scale, topk_idx, topk_w};

@@ -2330,6 +2330,12 @@ static ms_status sample_launch(SampleArgs a, ms_dtype dt, bool verify, cudaStrea
 // Rows and vocabulary that one launch can take.
 static bool sample_size_ok(long rows, int V) { return V <= SP_MAX_V && rows <= (1L << 24); }
 
+// Every pointer of a call at a multiple of its element (a load elsewhere would fault).
+static bool sample_aligned(const SampleArgs& a, ms_dtype dt) {
+    return element_aligned(a.logits, dt) && words_aligned(a.temperature, a.top_p, a.min_p, a.u, a.top_k, a.draft, a.q,
+                                                          a.token, a.probs);
+}
+
 }  // namespace ms
 
 extern "C" ms_status spec_sample(const void* logits, ms_dtype logits_dtype, int T, int V, const float* temperature,
@@ -2338,8 +2344,6 @@ extern "C" ms_status spec_sample(const void* logits, ms_dtype logits_dtype, int 
     if (!logits || !u || !token) return MS_ERR_INVALID_ARG;
     if (T <= 0 || V <= 0) return MS_ERR_INVALID_ARG;
     if (logits_dtype != MS_F32 && logits_dtype != MS_BF16) return MS_ERR_INVALID_ARG;
-    if (!ms::element_aligned(logits, logits_dtype)) return MS_ERR_INVALID_ARG;
-    if (!ms::sample_size_ok(T, V)) return MS_ERR_UNSUPPORTED;
     ms::SampleArgs a{};
     a.logits = logits;
     a.V = V;
@@ -2352,6 +2356,8 @@ extern "C" ms_status spec_sample(const void* logits, ms_dtype logits_dtype, int 
     a.u = u;
     a.token = token;
     a.probs = probs;
+    if (!ms::sample_aligned(a, logits_dtype)) return MS_ERR_INVALID_ARG;
+    if (!ms::sample_size_ok(T, V)) return MS_ERR_UNSUPPORTED;
     return ms::sample_launch(a, logits_dtype, false, static_cast<cudaStream_t>(stream));
 }
 
@@ -2362,13 +2368,9 @@ extern "C" ms_status spec_verify_sample(const void* logits, ms_dtype logits_dtyp
     if (!logits || (K > 0 && !draft) || !u || !committed || !n_committed) return MS_ERR_INVALID_ARG;
     if (B <= 0 || V <= 0 || K < 0) return MS_ERR_INVALID_ARG;
     if (logits_dtype != MS_F32 && logits_dtype != MS_BF16) return MS_ERR_INVALID_ARG;
-    if (!ms::element_aligned(logits, logits_dtype)) return MS_ERR_INVALID_ARG;
-    if (K > 8 || !ms::sample_size_ok(static_cast<long>(B) * (K + 1), V)) return MS_ERR_UNSUPPORTED;
     ms::SampleArgs a{};
     a.logits = logits;
     a.V = V;
-    a.rows = B * (K + 1);
-    a.per = K + 1;
     a.temperature = temperature;
     a.top_k = top_k;
     a.top_p = top_p;
@@ -2377,6 +2379,10 @@ extern "C" ms_status spec_verify_sample(const void* logits, ms_dtype logits_dtyp
     a.draft = draft;
     a.q = K > 0 ? draft_probs : nullptr;
     a.token = committed;
+    if (!ms::sample_aligned(a, logits_dtype) || !ms::words_aligned(n_committed)) return MS_ERR_INVALID_ARG;
+    if (K > 8 || !ms::sample_size_ok(static_cast<long>(B) * (K + 1), V)) return MS_ERR_UNSUPPORTED;
+    a.rows = B * (K + 1);
+    a.per = K + 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const ms_status st = ms::sample_launch(a, logits_dtype, true, s);
     if (st != MS_OK) return st;

@@ -51,6 +51,30 @@ def test_route_grouped_refusals(ms, change, code):
                                       a["k"], 1, 1.0, a["idx"], a["w"], None) == code
 
 
+@pytest.mark.parametrize("off", [1, 2, 3])
+@pytest.mark.parametrize("at", range(7))
+def test_sample_refuses_pointers_between_elements(ms, at, off):
+    p = [P(4096)] * 7   # temperature, top_k, top_p, min_p, u, token, probs
+    p[at] = P(4096 + off)
+    assert ms.lib().spec_sample(FAKE, 1, 4, 1000, *p, None) == -1
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+@pytest.mark.parametrize("at", range(9))
+def test_verify_sample_refuses_pointers_between_elements(ms, at, off):
+    p = [P(4096)] * 9   # draft, draft_probs, temperature, top_k, top_p, min_p, u, committed, n_committed
+    p[at] = P(4096 + off)
+    assert ms.lib().spec_verify_sample(FAKE, 0, *p[:7], 2, 3, 1000, *p[7:], None) == -1
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+@pytest.mark.parametrize("at", range(3))
+def test_route_grouped_refuses_pointers_between_elements(ms, at, off):
+    p = [P(4096)] * 3   # bias, topk_idx, topk_w
+    p[at] = P(4096 + off)
+    assert ms.lib().moe_route_grouped(FAKE, 0, p[0], 4, 64, 1, 8, 4, 2, 6, 1, 1.0, p[1], p[2], None) == -1
+
+
 def test_binding_refuses_tensors_it_cannot_take(ms):
     z = torch.zeros(2, 8)
     with pytest.raises(ValueError):
