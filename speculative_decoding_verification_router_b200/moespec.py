@@ -157,6 +157,15 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _outputs(stream, dev, *specs):
+    """New tensors of (dtype, shape) each; they belong to the stream that writes them, so that memory still in use on
+    another one is not handed out."""
+    if stream is None:
+        return [torch.empty(shape, dtype=dtype, device=dev) for dtype, shape in specs]
+    with torch.cuda.stream(stream):
+        return [torch.empty(shape, dtype=dtype, device=dev) for dtype, shape in specs]
+
+
 def _launch(fn, where: str, dev, stream, *args):
     """Calls fn(*args, stream) with dev current, on its current stream unless one is given."""
     s = _current_stream(dev.index) if stream is None else stream.cuda_stream
@@ -284,8 +293,7 @@ def route_grouped(logits: torch.Tensor, k: int, score: str = "softmax", bias: Op
     dev = logits.device
     bias_p = None if bias is None else _vec(bias, torch.float32, (E,), "bias", dev)
     if out is None:
-        idx = torch.empty(T, k, dtype=torch.int32, device=dev)
-        w = torch.empty(T, k, dtype=torch.float32, device=dev)
+        idx, w = _outputs(stream, dev, (torch.int32, (T, k)), (torch.float32, (T, k)))
         idx_p, w_p = idx.data_ptr(), w.data_ptr()
     else:
         idx, w = out
@@ -390,10 +398,10 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     filters = _filters(T, dev, temperature, top_k, top_p, min_p)
     probs_p = None
     if out is None:
-        token = torch.empty(T, dtype=torch.int32, device=dev)
+        token, *rest = _outputs(stream, dev, (torch.int32, (T,)), *([(torch.float32, (T, V))] if return_probs else []))
         token_p = token.data_ptr()
         if return_probs:
-            probs = torch.empty(T, V, dtype=torch.float32, device=dev)
+            probs, = rest
             probs_p = probs.data_ptr()
     else:
         token, probs = out if return_probs else (out, None)
@@ -419,8 +427,7 @@ def verify_sample(logits: torch.Tensor, draft: torch.Tensor, u: torch.Tensor, te
     filters = _filters(B, dev, temperature, top_k, top_p, min_p)
     q_p = None if draft_probs is None else _vec(draft_probs, torch.float32, (B, K, V), "draft_probs", dev)
     if out is None:
-        cm = torch.empty(B, K1, dtype=torch.int32, device=dev)
-        n = torch.empty(B, dtype=torch.int32, device=dev)
+        cm, n = _outputs(stream, dev, (torch.int32, (B, K1)), (torch.int32, (B,)))
         cm_p, n_p = cm.data_ptr(), n.data_ptr()
     else:
         cm, n = out

@@ -373,6 +373,26 @@ def test_two_streams_at_once(ms):
         assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
 
 
+def test_outputs_belong_to_the_stream_that_writes_them(ms):
+    """Memory freed on the current stream may still be in use there: a call on another stream must not be given it."""
+    R, V, E, s = 640, 64, 64, torch.cuda.Stream()
+    z, u = torch.randn(R, V, device="cuda"), torch.rand(R, device="cuda")
+    zv, uv = z.view(R // 4, 4, V), u.view(R // 4, 4)
+    d = torch.zeros(R // 4, 3, dtype=torch.int32, device="cuda")
+    calls = [lambda: ms.sample(z, u, return_probs=True, stream=s), lambda: ms.verify_sample(zv, d, uv, stream=s),
+             lambda: ms.route_grouped(z, 1, stream=s)]
+    want = [ms.sample(z, u, return_probs=True), ms.verify_sample(zv, d, uv), ms.route_grouped(z, 1)]
+    torch.cuda.synchronize()
+    for call, w in zip(calls, want):
+        freed = [torch.empty_like(x) for x in w for _ in range(3)]
+        at = {x.data_ptr() for x in freed}
+        del freed
+        out = call()
+        torch.cuda.synchronize()
+        assert not any(x.data_ptr() in at for x in out)
+        assert all(torch.equal(x, y) for x, y in zip(out, w))
+
+
 # ---------------------------------------------------------------- verification
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
