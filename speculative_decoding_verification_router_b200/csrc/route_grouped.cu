@@ -420,30 +420,31 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
             odd |= a.sigmoid ? lowest > kFar || lowest < -30.f : lowest - m < -80.f;
             ties = fabsf(lowest) < kTiny;
         } else {
-            // The scores of the lane's two best, in fp32 from their logits.  One is off by at most ev: by sigmoid
-            // 2.6e-7, by softmax 3.7e-6 of itself (most of it the sum's) and 5e-8 of the largest, with a bias two
-            // roundings more.  Where the second and third keys are not told apart, the third and fourth may be the
-            // larger ones, each by at most disp, a step of the keys (2^-15 relative).  A group's sum has two scores of
-            // any of its lanes, and a comparison two groups, of which the one left out may lack two displaced ones:
-            // 4 ev + 2 disp, and twice that, as the lane with the largest ev need not be the one with the largest disp.
+            // The scores of the lane's two best, in fp32 from their logits, then of its group's, in every lane of it.
+            // Errors: a score's own, 2.6e-7 by sigmoid, by softmax 3e-7 of itself and 5e-8 of the largest; the fp32
+            // sum's, 3.4e-6 of a score by softmax (without a bias the same for all); a rounding of every sum.  Where
+            // the second and third keys of a lane are not told apart, the third and fourth may be the larger ones,
+            // each by at most disp, a step of the keys (2^-15 relative).  A comparison has four scores, and the group
+            // left out may lack two displaced ones.  r: for groups of errors x and y and displacement d of the second,
+            // max(2 x, 2 y + 4 d) >= x + y + 2 d, so the largest r of all lanes covers two groups; doubled where the
+            // scores' part varies as well.
             const TL* row = static_cast<const TL*>(a.logits) + static_cast<size_t>(t) * a.E;
             const int e1 = 255 - (best[0] & 255), e2 = P > 1 ? 255 - (best[1] & 255) : e1;
             const float z1 = rg_load(row + e1), z2 = rg_load(row + e2);
             odd |= a.sigmoid ? fabsf(z1) > 30.f : z1 - m < -80.f;
             float c1 = a.sigmoid ? rg_rcp(1.f + rg_ex2(z1 * -kLog2e)) : rg_ex2((z1 - m) * kLog2e) * norm;
             float c2 = a.sigmoid ? rg_rcp(1.f + rg_ex2(z2 * -kLog2e)) : rg_ex2((z2 - m) * kLog2e) * norm;
-            float ev = a.sigmoid ? 2.6e-7f : fmaf(fmaxf(c1, c2), 3.7e-6f, 5e-8f * norm), disp = 0.f;
+            float err = a.sigmoid ? 1.04e-6f : a.bias ? fmaf(fmaxf(c1, c2), 1.7e-5f, 4e-7f * norm) : 2e-7f * norm;
+            float disp = 0.f;
             if (a.bias) {
                 c1 += __ldg(a.bias + e1);
                 c2 += __ldg(a.bias + e2);
-                ev += 1.2e-7f * fmaxf(fabsf(c1), fabsf(c2));
                 odd |= !(c1 == c1);   // a NaN bias: the lane's first key, and comparisons with it would lose its group
             }
             if (P > 2 && rg_value(best[1] & ~255) - rg_value(best[2] & ~255) <= fabsf(rg_value(best[1] & ~255)) * 4e-5f + 8e-6f) {
                 disp = a.bias ? fabsf(c2) * 3.2e-5f : fabsf(z2) * (a.sigmoid ? 1e-5f : 4e-5f * c2);
                 odd |= !(fabsf(z2) < 1e4f);   // a step of the logit is more than a small part of its weight
             }
-            float err = 8.f * ev + 4.f * disp;
             if (P == 1) c2 = -INFINITY;
             // equal keys come to the lower expert first, which may have the smaller score
             const float larger = fmaxf(c1, c2);
@@ -453,6 +454,9 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
                 const float o1 = __shfl_xor_sync(0xffffffffu, c1, o), o2 = __shfl_xor_sync(0xffffffffu, c2, o);
                 merge_two(c1, c2, o1, o2);
             }
+            const float both = fabsf(c1) + (a.E == a.groups ? 0.f : fabsf(c2));
+            const float r = fmaf(both, a.sigmoid || a.bias ? 2.4e-7f : 7.2e-7f, 4.f * disp);
+            err += a.sigmoid || !a.bias ? r : 2.f * r;
             const float g = a.group_top == 2 && c2 > -INFINITY ? c1 + c2 : c1;
             int better = 0;
 #pragma unroll
@@ -496,10 +500,12 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
     if (!a.bias) {
         close |= sizeof(TL) == 4 && next != kNoKey && ((kth ^ next) & ~255) == 0;
         ties |= fabsf(rg_value(kth & ~255)) < kTiny;
-        if (ties) {
-#pragma unroll
-            for (int i = 0; i < NL * 8; ++i)
-                if (FULL || i < P) odd |= fabsf(zval(i)) < kTiny && zval(i) != 0.f;
+        if (ties) {   // (seldom: read again)
+#pragma unroll 1
+            for (int i = 0; i < P; ++i) {
+                const float zi = rg_load(zr + i);
+                odd |= fabsf(zi) < kTiny && zi != 0.f;
+            }
         }
     } else if (next != kNoKey) {
         const float vk = rg_value(kth & ~255), vn = rg_value(next & ~255);
@@ -650,7 +656,8 @@ extern "C" ms_status moe_route_grouped(const void* logits, ms_dtype logits_dtype
     if (T <= 0 || E <= 0 || n_groups <= 0 || E % n_groups != 0) return MS_ERR_INVALID_ARG;
     if (topk_groups <= 0 || topk_groups > n_groups || group_top < 1 || group_top > 2) return MS_ERR_INVALID_ARG;
     if (k <= 0 || k > topk_groups * (E / n_groups)) return MS_ERR_INVALID_ARG;
-    if (!ms::element_aligned(logits, logits_dtype) || !ms::words_aligned(select_bias, topk_idx, topk_w)) return MS_ERR_INVALID_ARG;
+    if (!ms::element_aligned(logits, logits_dtype)) return MS_ERR_INVALID_ARG;
+    if (!ms::words_aligned(select_bias, topk_idx, topk_w)) return MS_ERR_INVALID_ARG;
     if (E > ms::RG_MAXE || n_groups > 32 || k > 32) return MS_ERR_UNSUPPORTED;
     ms::RouteGroupedArgs a{logits,       select_bias,  T,     E,        n_groups, topk_groups, group_top, k,
                            score == MS_SIGMOID, renormalize != 0, scale, topk_idx, topk_w};
