@@ -152,18 +152,18 @@ def _filters(n: int, dev, temperature, top_k, top_p, min_p):
             None if min_p is None else _vec(min_p, torch.float32, shape, "min_p", dev))
 
 
+def _empty(stream, dev, dtype, *shape):
+    """A new output.  It belongs to the stream that writes it, so that memory still in use on another one is not
+    handed out.  (Sizes one by one: as a tuple they cost the call 2 us.)"""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=dev)
+
+
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _outputs(stream, dev, *specs):
-    """New tensors of (dtype, shape) each; they belong to the stream that writes them, so that memory still in use on
-    another one is not handed out."""
-    if stream is None:
-        return [torch.empty(shape, dtype=dtype, device=dev) for dtype, shape in specs]
-    with torch.cuda.stream(stream):
-        return [torch.empty(shape, dtype=dtype, device=dev) for dtype, shape in specs]
 
 
 def _launch(fn, where: str, dev, stream, *args):
@@ -293,7 +293,8 @@ def route_grouped(logits: torch.Tensor, k: int, score: str = "softmax", bias: Op
     dev = logits.device
     bias_p = None if bias is None else _vec(bias, torch.float32, (E,), "bias", dev)
     if out is None:
-        idx, w = _outputs(stream, dev, (torch.int32, (T, k)), (torch.float32, (T, k)))
+        idx = _empty(stream, dev, torch.int32, T, k)
+        w = _empty(stream, dev, torch.float32, T, k)
         idx_p, w_p = idx.data_ptr(), w.data_ptr()
     else:
         idx, w = out
@@ -398,10 +399,10 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     filters = _filters(T, dev, temperature, top_k, top_p, min_p)
     probs_p = None
     if out is None:
-        token, *rest = _outputs(stream, dev, (torch.int32, (T,)), *([(torch.float32, (T, V))] if return_probs else []))
+        token = _empty(stream, dev, torch.int32, T)
         token_p = token.data_ptr()
         if return_probs:
-            probs, = rest
+            probs = _empty(stream, dev, torch.float32, T, V)
             probs_p = probs.data_ptr()
     else:
         token, probs = out if return_probs else (out, None)
@@ -427,7 +428,8 @@ def verify_sample(logits: torch.Tensor, draft: torch.Tensor, u: torch.Tensor, te
     filters = _filters(B, dev, temperature, top_k, top_p, min_p)
     q_p = None if draft_probs is None else _vec(draft_probs, torch.float32, (B, K, V), "draft_probs", dev)
     if out is None:
-        cm, n = _outputs(stream, dev, (torch.int32, (B, K1)), (torch.int32, (B,)))
+        cm = _empty(stream, dev, torch.int32, B, K1)
+        n = _empty(stream, dev, torch.int32, B)
         cm_p, n_p = cm.data_ptr(), n.data_ptr()
     else:
         cm, n = out
