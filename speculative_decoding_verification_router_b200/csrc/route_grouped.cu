@@ -442,7 +442,9 @@ __global__ void __launch_bounds__(RG_WARPS * 32, NL == 4 ? 3 : 4)
                 odd |= !(c1 == c1);   // a NaN bias: the lane's first key, and comparisons with it would lose its group
             }
             if (P > 2 && rg_value(best[1] & ~255) - rg_value(best[2] & ~255) <= fabsf(rg_value(best[1] & ~255)) * 4e-5f + 8e-6f) {
-                disp = a.bias ? fabsf(c2) * 3.2e-5f : fabsf(z2) * (a.sigmoid ? 1e-5f : 4e-5f * c2);
+                // (by softmax with a bias their scores may be any, and so their part of the sum's error)
+                disp = a.bias ? fmaf(fabsf(c2), 3.2e-5f, a.sigmoid ? 0.f : 2e-6f)
+                              : fabsf(z2) * (a.sigmoid ? 1e-5f : 4e-5f * c2);
                 odd |= !(fabsf(z2) < 1e4f);   // a step of the logit is more than a small part of its weight
             }
             if (P == 1) c2 = -INFINITY;

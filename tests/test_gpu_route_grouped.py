@@ -276,6 +276,23 @@ def test_softmax_sum_that_rounds_one_way(ms):
         _check(ms, z, 2, "f32", bias=bias, score="softmax")
 
 
+def test_softmax_sum_that_rounds_one_way_in_a_group(ms):
+    """The same row: the largest score, nearly taken back by its bias, is its group's best by less than the sum's error
+    and comes third by its key; another group's two lie in between."""
+    E = 256
+    z = np.full((1, E), -40.0, np.float32)
+    z[0, :32] = np.float32(np.log(6.05e-8))
+    z[0, 2] = 0.0
+    s = 1 / np.exp(z[0].astype(np.float64)).sum()
+    for over in (1.0e-6, 1.3e-6, 1.6e-6):
+        for between in (0.6, 0.75, 0.9):
+            bias = np.float32(-1e-3) - np.float32(2e-5) * np.arange(E, dtype=np.float32)   # (no other close scores)
+            bias[[0, 1]] = 1e-3
+            bias[2] = 1e-3 + over - s
+            bias[[32, 33]] = 1e-3 + between * over / 2
+            _check(ms, z, 2, "f32", bias=bias, score="softmax", n_groups=8, topk_groups=1, group_top=2)
+
+
 def test_softmax_without_groups_is_route_topk(ms):
     g = np.random.default_rng(1)
     H, E, T = 256, 64, 50
