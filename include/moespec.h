@@ -125,12 +125,12 @@ MS_API ms_status moe_route_topk_tensor(const void* xhat, const float* w_router, 
  * The choice is that of scores in fp64: it does not depend on fp32 rounding.
  * Different logits whose fp64 scores are equal (sigmoid of large ones, logits
  * around zero that differ by less than 1e-16) are equal values.
- * topk_w is evaluated in fp32 (about 1e-6 relative).  A logit of -inf or NaN
- * masks its expert: s = 0, ranked behind every other expert of the chosen
- * groups (a masked expert counts 0 in its group's score, a group without any
- * other expert ranks last), so that topk_idx always holds k different experts
- * of the chosen groups, as moe_permute needs.  A bias of -inf or NaN ranks its
- * expert with the masked ones and leaves it its s.
+ * topk_w is evaluated in fp32 (about 1e-6 relative, 4e-6 at most).  A logit of
+ * -inf or NaN masks its expert: s = 0, ranked behind every other expert of the
+ * chosen groups (a masked expert counts 0 in its group's score, a group without
+ * any other expert ranks last), so that topk_idx always holds k different
+ * experts of the chosen groups, as moe_permute needs.  A bias of -inf or NaN
+ * ranks its expert with the masked ones and leaves it its s.
  * logits: [T,E] fp32 or bf16 (any element alignment).  select_bias: [E] fp32
  * or NULL.  topk_idx: [T,k] int32.  topk_w: [T,k] fp32.
  * E <= 256, E % n_groups == 0, n_groups <= 32, k <= 32,
@@ -251,8 +251,10 @@ MS_API ms_status spec_verify_greedy(const void* logits, ms_dtype logits_dtype, c
  * cumulative kept weight exceeds u[r] times the sum of the kept weights.
  * probs[r,v] = w_v / that sum, 0 where not kept (what spec_verify_sample takes
  * as draft_probs).
- * Weights and sums are computed beyond fp32 (about 1e-13, fixed order), so a
- * token does not depend on rounding, the batch or the run.
+ * Weights are computed to about 1e-13 and summed in fp64, in an order that
+ * follows V and the number of rows: the token is the exact one unless u[r]
+ * times the sum lies within about 1e-12 of a border, and it is the same in every
+ * run.  probs are rounded to fp32 once; the last bit may differ between batches.
  * A temperature that is not above 0 (0, negative, NaN) makes its row greedy:
  * the lowest index among the largest logits.  top_k <= 0 or >= V, top_p >= 1
  * or NaN, min_p <= 0 or NaN leave their filter out; min_p > 1 counts as 1,

@@ -15,16 +15,16 @@
 // in the low bits of the same word), proves that the set is right by the gap
 // behind the k-th, and orders the k by their logits or fp32 scores.  Where that
 // gap, or one among the k, is within the scores' error, up to 16 contenders are
-// settled by fp64 scores; tokens with masked, infinite or far logits, and those
-// whose groups are not told apart, take the exact form.
+// settled by fp64 scores; tokens with masked, infinite, far or tiny logits, and
+// those whose groups are not told apart, take the exact form.
 //
 // What bounds it: the sorting networks (minimum and maximum at half the rate of
 // an add) and, in a launch of a few waves, the tail of its last blocks; memory
 // asks for a tenth of the time.  Measured (replayed in a graph):
-//   128 tokens, 64 experts, fp32, bias               4.4 us
-//   36,992 tokens, 64 experts, fp32, 8 groups       14.2 us  (0.79 TB/s)
-//   8,191 tokens, 256 experts, fp32, bias, groups   15.7 us  (0.57 TB/s)
-//   36,992 tokens, 256 experts, bf16, bias, groups  28.3 us  (0.75 TB/s)
+//   128 tokens, 64 experts, fp32, bias               4.3 us
+//   36,992 tokens, 64 experts, fp32, 8 groups       13.6 us  (0.83 TB/s)
+//   8,191 tokens, 256 experts, fp32, bias, groups   15.9 us  (0.56 TB/s)
+//   36,992 tokens, 256 experts, bf16, bias, groups  29.0 us  (0.73 TB/s)
 // (The parameters are __grid_constant__: the exact form takes them by reference,
 // and a copy of them in every thread's local memory costs 6 % of that.)
 #include <limits.h>
@@ -212,7 +212,7 @@ __device__ __noinline__ void route_token_exact(const RouteGroupedArgs& a, int t,
 
 // Any shape, in the exact form: one warp per token.  It is for the shapes that
 // the fast form cannot take: 36,992 tokens of 64 and of 256 experts took 62 and
-// 121 us by it, 14 and 28 by the other.
+// 121 us by it, 14 and 29 by the other.
 template <typename TL>
 __global__ void __launch_bounds__(RG_WARPS * 32) route_grouped_kernel(const __grid_constant__ RouteGroupedArgs a) {
     __shared__ double sel[RG_WARPS][RG_MAXE];

@@ -32,11 +32,11 @@
 // element and fp64 pass, 11 of them fp64 at two issue cycles.  Memory is not the
 // bound: the row is read once.  Measured at V = 129,280 (replayed in a graph):
 //   1 bf16 row, all filters                       7.7 us
-//   32 fp32 rows, top-p (3 of them wide)           50 us
-//   64 bf16 rows, temperature, probs written       36 us  (1.4 TB/s)
-//   512 bf16 rows, filters of every kind          131 us  (1.0 TB/s)
-//   verification of 32 x 4 bf16 rows, top-p        91 us
-//   the same by temperature with draft probs       63 us  (0.8 TB/s)
+//   32 fp32 rows, top-p (3 of them wide)           52 us
+//   64 bf16 rows, temperature, probs written       39 us  (1.3 TB/s)
+//   512 bf16 rows, filters of every kind          129 us  (1.0 TB/s)
+//   verification of 32 x 4 bf16 rows, top-p        88 us
+//   the same by temperature with draft probs       62 us  (0.8 TB/s)
 #include <float.h>
 #include <limits.h>
 #include <math.h>
